@@ -283,7 +283,7 @@ def _plan(s):
     before_p, after_p = (lens.long() + page - 1) // page, (after + page - 1) // page
     new, pops, pushes = delta.long().clamp(min=0), (after_p - before_p).clamp(min=0), (before_p - after_p).clamp(min=0)
     ends, pop_ends, push_ends = new.cumsum(0), pops.cumsum(0), pushes.cumsum(0)
-    books = (head < 0) | (head >= num_pages) | (count < 0) | (count > num_pages) | (count - pop_ends[-1] + push_ends[-1] > num_pages)
+    books = (head < 0) | (head >= num_pages) | (count < 0) | (count > num_pages) | (count + push_ends[-1] > num_pages)
     verdict = (SHORT * (pop_ends[-1] > count) + BAD_LENGTH * ((lens < 0) | (after < 0) | (after > width * page)).any()
                + CAPACITY * (ends[-1] > cap) + BAD_STATE * books)
     ok = verdict == 0
