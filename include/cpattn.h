@@ -64,10 +64,14 @@ typedef enum {
     CPATTN_ERR_ALIGN = 4,     /* a pointer is not 16-byte aligned */
     CPATTN_ERR_CUDA = 5,      /* a CUDA runtime call or launch failed */
     CPATTN_ERR_TIMEOUT = 6,   /* a bounded in-kernel wait ran out (reported later) */
-    CPATTN_ERR_WORKSPACE = 7  /* workspace missing or smaller than required */
+    CPATTN_ERR_WORKSPACE = 7, /* workspace missing or smaller than required */
+    CPATTN_ERR_PAGE = 8       /* a page number, slot or length outside of the paged cache (reported later) */
 } cpattn_status;
 
 typedef enum { CPATTN_BF16 = 0, CPATTN_FP32 = 1 } cpattn_dtype;
+
+/* Element type of a paged cache beside the two above: e4m3 codes. */
+enum { CPATTN_E4M3 = 2 };
 
 /* Block kinds in a plan row. */
 enum { CPATTN_SKIP = 0, CPATTN_FULL = 1, CPATTN_DIAG = 2 };
@@ -322,9 +326,132 @@ int cpattn_gemm(const void* A, const void* B, const void* bias, void* C, int M, 
                 int a_layout, int b_layout, void* stream);
 
 /*
+ * The paged key-value cache: answering, token by token, from the long contexts
+ * that the calls above train on and prefill.
+ *
+ *   k_cache, v_cache  [num_pages][Hkv][page_size][D] of cache_dtype: CPATTN_BF16
+ *                     or CPATTN_FP32 with q, k, v of the same dtype, or
+ *                     CPATTN_E4M3 (one byte per element) with bf16 q, k, v.
+ *                     page_size is 16, 32, 64, 128 or 256; D is 64 or 128.
+ *   k_bounds          [num_pages][Hkv][2][D] of cache_dtype: elementwise smallest
+ *                     (row 0) and largest (row 1) key of each page, as stored
+ *   kv_amax           device float[2], max|k| and max|v| that an e4m3 cache is
+ *                     scaled by: code = e4m3(fp32(x * s)), s = 448 / amax, saturating
+ *                     (as cpattn_quantize_e4m3); NULL for the other types
+ *   lens              [R] int32: tokens of request r that the cache holds
+ *   block_table       [R][max_pages] int32: the page of tokens j * page_size ..
+ *                     is block_table[r][j]; entries behind the last held page are
+ *                     never read
+ *   slot              page * page_size + row, int64: where one token's rows stand
+ * Positions behind a request's length may hold anything, NaN included: they are
+ * never part of a result.  R requests of which some have length 0 are a padded
+ * batch.  A page number, slot or length outside of its range is not followed:
+ * the rows it stands for are left out and CPATTN_ERR_PAGE is recorded in the
+ * device error word (cpattn_sync_status).  All sizes are read on the device, so
+ * every call can be captured into a CUDA graph and replayed as lengths change.
+ * Limits (CPATTN_ERR_SHAPE): max_pages * page_size < 2^31, at most 64 query
+ * heads per kv head (Hq % Hkv == 0).
+ */
+
+/* Bits of a plan's verdict. */
+enum {
+    CPATTN_PLAN_SHORT = 1,      /* fewer free pages than the step needs */
+    CPATTN_PLAN_BAD_LENGTH = 2, /* a length would fall below 0 or pass max_pages * page_size */
+    CPATTN_PLAN_CAPACITY = 4,   /* more new tokens than `capacity` slots */
+    CPATTN_PLAN_BAD_STATE = 8   /* the free pages' books do not balance */
+};
+
+/*
+ * cpattn_cache_plan -- the books of one step, on the device.
+ *   delta          [R] int32: new tokens of request r (> 0), or minus the tokens
+ *                  to take back (< 0: rejected drafts, or -lens[r] for a request that ends)
+ *   free_ring      [num_pages] int32, free_state int32[2] = {head, count}: the free
+ *                  pages are free_ring[(head + i) % num_pages], i < count; taken
+ *                  from the front, returned behind the last, requests in order
+ *   lens_out       [R], free_state_out [2]: the new lengths and state (written);
+ *                  may be the same memory as lens and free_state.  With other
+ *                  memory the call can be repeated and gives the same again
+ *   block_table, free_ring: entries of pages taken and returned are written, the
+ *                  others (those of returned pages too) left as they are
+ *   cu_new         [R + 1]: first new token of request r in the packed order
+ *   slots          [capacity] int64: slot of every new token, -1 behind the last
+ *   verdict        int32[1]: 0, or CPATTN_PLAN_* bits; then nothing changes:
+ *                  lens_out = lens, free_state_out = free_state, cu_new 0, slots -1
+ * Pages returned by a call can be taken from the next call on.
+ * Workspace: cpattn_cache_plan_workspace_bytes(R), 16-byte aligned; contents on
+ * entry are ignored; calls that can overlap on the GPU need one each.
+ */
+size_t cpattn_cache_plan_workspace_bytes(int R);
+int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_table, int R,
+                      int max_pages, int page_size, int32_t* free_ring, const int32_t* free_state,
+                      int num_pages, int32_t* lens_out, int32_t* free_state_out, int32_t* cu_new,
+                      int64_t* slots, long capacity, int32_t* verdict, void* workspace,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * cpattn_cache_append -- rows k_new[i][h][:], v_new[i][h][:] (i < N, h < Hkv) into
+ * slots[i] of the cache; negative slots are skipped.
+ *   strides        of tokens and heads in elements, multiples of 16 bytes
+ *                  (CPATTN_ERR_SHAPE); columns are contiguous.  K and V as the layer
+ *                  saves them ([H][S][D]) have token stride D and head stride S * D
+ *   k_bounds       kept up to date, or NULL.  A row in a page's first slot starts
+ *                  the page's bounds afresh.  With k_bounds, the new tokens of one
+ *                  page must stand next to one another and ascend, as
+ *                  cpattn_cache_plan lists them.  Bounds do not shrink when tokens are
+ *                  taken back: they still cover the rows that were there
+ * A slot may appear once only.  N = 0 does nothing.
+ */
+int cpattn_cache_append(const void* k_new, const void* v_new, long k_tok_stride, long k_head_stride,
+                        long v_tok_stride, long v_head_stride, const int64_t* slots, long N,
+                        void* k_cache, void* v_cache, void* k_bounds, int Hkv, int D, int page_size,
+                        int num_pages, const float* kv_amax, int dtype, int cache_dtype, void* stream);
+
+/*
+ * cpattn_select_pages -- the pages that one new token per request attends to when
+ * the context is too long to read whole.  For kv head h and page j
+ *     score = max over the group's query heads i of sum_d max(q_id lo_d, q_id hi_d),
+ * an upper bound of q.k over the page, summed in 64 bits and rounded to fp32.
+ *   q              [R][Hq][D] dtype
+ *   pages          [R][Hkv][budget] int32 (written): the `budget` pages with the
+ *                  largest scores, ascending, ties to the lower page, -1 behind the
+ *                  last; the newest page and the first keep_first pages are always
+ *                  among them.  All pages where a request has no more than budget
+ * Preconditions: budget > keep_first >= 0, max_pages <= 262144.
+ */
+int cpattn_select_pages(const void* q, const void* k_bounds, const int32_t* block_table,
+                        const int32_t* lens, int32_t* pages, int R, int Hq, int Hkv, int D,
+                        int page_size, int max_pages, int num_pages, int budget, int keep_first,
+                        int dtype, int cache_dtype, void* stream);
+
+/*
+ * cpattn_decode -- attention of one new token per request over its cached keys:
+ *     o = sum_j softmax_j(scale * q . k_j) v_j,  lse = log sum_j exp(scale * q . k_j)
+ * over the lens[r] tokens of request r (the new token's own among them once it is
+ * appended), or over those in the listed pages.  Query head i reads kv head
+ * i / (Hq / Hkv).
+ *   q              [R][Hq][D] dtype
+ *   pages          NULL, or [R][Hkv][budget] int32 as cpattn_select_pages writes it:
+ *                  the first min(budget, held pages) entries are read, negative
+ *                  ones are skipped, a page listed twice counts twice
+ *   o              [R][Hq][D] of o_dtype (CPATTN_BF16 or CPATTN_FP32); lse [R][Hq] fp32.
+ *                  Requests without a key: o = 0, lse = -inf.  fp32 results of
+ *                  parts of one context (kept by several ranks) are combined by
+ *                  cpattn_merge and rounded by cpattn_finalize
+ * Workspace: cpattn_decode_workspace_bytes(R, Hq, Hkv, D) (0 for invalid sizes),
+ * 256-byte aligned; contents on entry are ignored; calls that can overlap on the
+ * GPU need one each.  Results do not depend on it, nor on other requests' values.
+ */
+size_t cpattn_decode_workspace_bytes(int R, int Hq, int Hkv, int D);
+int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_table, const int32_t* lens, const int32_t* pages, void* o,
+                  float* lse, int R, int Hq, int Hkv, int D, int page_size, int max_pages,
+                  int num_pages, int budget, float scale, const float* kv_amax, void* workspace,
+                  size_t ws_bytes, int dtype, int cache_dtype, int o_dtype, void* stream);
+
+/*
  * cpattn_sync_status -- synchronises `stream`, then returns and clears the
- * device-side error word of the current device (CPATTN_OK, CPATTN_ERR_TIMEOUT)
- * or CPATTN_ERR_CUDA if the synchronisation itself failed.  The word's device
+ * device-side error word of the current device (CPATTN_OK, CPATTN_ERR_TIMEOUT,
+ * CPATTN_ERR_PAGE) or CPATTN_ERR_CUDA if the synchronisation itself failed.  The word's device
  * address is looked up once per device and kept: as for cpattn_bwd_noalloc,
  * do not use the library across a cudaDeviceReset in the same process.
  */
@@ -361,7 +488,9 @@ long long cpattn_launch_count(void);
  *   8 tcgen05 dQ, 9 layer head split / merge, 10 layer bias gradients,
  *   11 gradient accumulation (cpattn_accumulate), 12 GEMM (cpattn_gemm and
  *   the layer's projections), 13 tcgen05 e4m3 forward (cpattn_fwd_fp8),
- *   14 max|x| and e4m3 quantisation.
+ *   14 max|x| and e4m3 quantisation, 15 single-token attention over the paged
+ *   cache, 16 the join of its partial results, 17 page and slot planning, 18
+ *   append to the paged cache, 19 page selection.
  */
 int cpattn_profile(int on);
 int cpattn_profile_read(int kernel_kind, double* total_ms, long long* launches);

@@ -6,6 +6,7 @@ turns a non-zero status into an exception.  All arithmetic runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback.  If the shared
 library has not been built, importing this module raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -14,8 +15,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcpattn.so")
 
-OK, ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE = range(8)
+OK, ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_PAGE = range(9)
 BF16, FP32 = 0, 1
+E4M3 = 2  # element type of a paged cache only
+PLAN_SHORT, PLAN_BAD_LENGTH, PLAN_CAPACITY, PLAN_BAD_STATE = 1, 2, 4, 8  # bits of cache_plan's verdict
 SKIP, FULL, DIAG = 0, 1, 2
 PLAN_FIELDS = 6
 
@@ -26,7 +29,9 @@ EXPORTS = ["cpattn_plan", "cpattn_fwd", "cpattn_fwd_step", "cpattn_merge", "cpat
            "cpattn_debug_stall", "cpattn_profile", "cpattn_profile_read", "cpattn_bwd_noalloc",
            "cpattn_layer_workspace_bytes", "cpattn_layer_fwd", "cpattn_layer_bwd",
            "cpattn_accumulate", "cpattn_bwd_accumulate", "cpattn_gemm", "cpattn_amax",
-           "cpattn_quantize_e4m3", "cpattn_fwd_fp8"]
+           "cpattn_quantize_e4m3", "cpattn_fwd_fp8", "cpattn_cache_plan_workspace_bytes",
+           "cpattn_cache_plan", "cpattn_cache_append", "cpattn_select_pages",
+           "cpattn_decode_workspace_bytes", "cpattn_decode"]
 
 # size of the library's fixed scratch array behind bwd_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -70,6 +75,12 @@ def _load():
         "cpattn_quantize_e4m3": ([vp, i, i, i, i, i, vp, vp, vp], i),
         "cpattn_fwd_fp8": ([vp] * 6 + [i] * 6 + [f, vp], i),
         "cpattn_layer_bwd": ([vp] * 14 + [i] * 6 + [f, vp, sz, vp], i),
+        "cpattn_cache_plan_workspace_bytes": ([i], sz),
+        "cpattn_cache_plan": ([vp] * 3 + [i] * 3 + [vp] * 2 + [i] + [vp] * 4 + [l, vp, vp, sz, vp], i),
+        "cpattn_cache_append": ([vp] * 2 + [l] * 4 + [vp, l] + [vp] * 3 + [i] * 4 + [vp, i, i, vp], i),
+        "cpattn_select_pages": ([vp] * 5 + [i] * 11 + [vp], i),
+        "cpattn_decode_workspace_bytes": ([i] * 4, sz),
+        "cpattn_decode": ([vp] * 8 + [i] * 8 + [f, vp, vp, sz, i, i, i, vp], i),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -469,6 +480,193 @@ def layer_bwd(x, w_qkv, w_o, saved, dy, num_heads: int, cp_size: int, causal: bo
     return dx, dw_qkv, db_qkv, dw_o, db_o
 
 
+def _cache(k_cache, kv_amax):
+    """Checks a paged cache tensor; returns (sizes, rows' dtype, dtype code)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [num_pages, kv_heads, page_size, D] tensor")
+    if k_cache.dtype == torch.uint8:
+        if kv_amax is None:
+            raise ValueError("kv_amax must be given for an e4m3 (uint8) cache")
+        _expect(kv_amax, "kv_amax", (2,), torch.float32, k_cache)
+        return k_cache.shape, torch.bfloat16, E4M3
+    if kv_amax is not None:
+        raise ValueError("kv_amax is for an e4m3 (uint8) cache only")
+    return k_cache.shape, k_cache.dtype, _dtype_code(k_cache)
+
+
+def _here(t: torch.Tensor, name: str):
+    """The paged cache's kernels start on the current device: `t` must be there."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _on(stream):
+    """Outputs and workspaces of a call are allocated for the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _batch(block_table, lens, like=None):
+    """Checks a page table [R, max_pages] and the lengths [R]."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a [R, max_pages] tensor")
+    _expect(block_table, "block_table", block_table.shape, torch.int32, like)
+    _expect(lens, "lens", block_table.shape[:1], torch.int32, block_table)
+    return block_table.shape
+
+
+def _query(q, dtype, R, heads, D, like):
+    """Checks q [R, Hq, D] against the cache it reads; returns Hq."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [R, Hq, D] tensor")
+    Hq = q.shape[1]
+    _expect(q, "q", (R, Hq, D), dtype, like)
+    if Hq % heads != 0:
+        raise ValueError(f"q has {Hq} heads, not a multiple of the cache's {heads}")
+    return Hq
+
+
+def cache_plan_workspace_bytes(R) -> int:
+    return int(lib.cpattn_cache_plan_workspace_bytes(R))
+
+
+def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, capacity: int,
+               lens_out=None, free_state_out=None, workspace=None, stream=None):
+    """The books of one step over a paged cache: request r takes delta[r] new
+    tokens, or gives -delta[r] back.  Writes block_table and free_ring; returns
+    (lens, free_state, cu_new, slots, verdict), all on the device: the new lengths
+    and free-page state (new tensors, or lens_out / free_state_out, which may be
+    lens and free_state themselves), the first new token of each request, the slot
+    of each new token (`capacity` of them, -1 behind the last) and 0 or PLAN_* bits
+    (then nothing changed)."""
+    R, max_pages = _batch(block_table, lens)
+    _expect(delta, "delta", (R,), torch.int32, block_table)
+    if not isinstance(free_ring, torch.Tensor) or free_ring.dim() != 1:
+        raise ValueError("free_ring must be a [num_pages] tensor")
+    _expect(free_ring, "free_ring", free_ring.shape, torch.int32, block_table)
+    _expect(free_state, "free_state", (2,), torch.int32, block_table)
+    if lens_out is not None:
+        _expect(lens_out, "lens_out", (R,), torch.int32, block_table)
+    if free_state_out is not None:
+        _expect(free_state_out, "free_state_out", (2,), torch.int32, block_table)
+    _here(block_table, "block_table")
+    need = cache_plan_workspace_bytes(R)
+    with _on(stream):
+        i32 = dict(dtype=torch.int32, device=block_table.device)
+        lens_out = torch.empty(R, **i32) if lens_out is None else lens_out
+        free_state_out = torch.empty(2, **i32) if free_state_out is None else free_state_out
+        cu_new, verdict = torch.empty(R + 1, **i32), torch.empty(1, **i32)
+        slots = torch.empty(max(0, capacity), dtype=torch.int64, device=block_table.device)
+        workspace = _workspace(workspace, need, block_table)
+        _check(lib.cpattn_cache_plan(_p(lens), _p(delta), _p(block_table), R, max_pages, page_size, _p(free_ring),
+                                     _p(free_state), free_ring.shape[0], _p(lens_out), _p(free_state_out),
+                                     _p(cu_new), _p(slots), capacity, _p(verdict), _p(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)),
+               "cpattn_cache_plan")
+    return lens_out, free_state_out, cu_new, slots, verdict
+
+
+def cache_append_(k_new, v_new, slots, k_cache, v_cache, k_bounds=None, kv_amax=None, stream=None):
+    """New rows into a paged cache (in place): k_new, v_new [N, kv_heads, D] with
+    contiguous columns (views of [kv_heads, N, D] too), slots [N] int64 (negative:
+    skipped).  k_bounds [num_pages, kv_heads, 2, D] is kept up to date when given."""
+    (num_pages, heads, page_size, D), dtype, code = _cache(k_cache, kv_amax)
+    _expect(k_cache, "k_cache", k_cache.shape, k_cache.dtype)
+    _expect(v_cache, "v_cache", k_cache.shape, k_cache.dtype, k_cache)
+    if k_bounds is not None:
+        _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_cache.dtype, k_cache)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a [N] tensor")
+    N = slots.shape[0]
+    _expect(slots, "slots", (N,), torch.int64, k_cache)
+    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if tuple(t.shape) != (N, heads, D):
+            raise ValueError(f"{n} must have shape {(N, heads, D)}, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
+        if t.device != k_cache.device:
+            raise ValueError(f"{n} is on {t.device}, expected {k_cache.device}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{n} must have contiguous columns")
+    _here(k_cache, "k_cache")
+    _check(lib.cpattn_cache_append(_p(k_new), _p(v_new), k_new.stride(0), k_new.stride(1), v_new.stride(0),
+                                   v_new.stride(1), _p(slots), N, _p(k_cache), _p(v_cache), _p(k_bounds), heads, D,
+                                   page_size, num_pages, _p(kv_amax), BF16 if dtype == torch.bfloat16 else FP32,
+                                   code, _stream(stream)), "cpattn_cache_append")
+    return k_cache, v_cache
+
+
+def select_pages(q, k_bounds, block_table, lens, page_size: int, budget: int, keep_first: int = 0, stream=None):
+    """The pages one new token per request attends to: int32 [R, kv_heads, budget],
+    ascending, -1 behind the last (see cpattn_select_pages in include/cpattn.h).
+    q [R, Hq, D]; k_bounds [num_pages, kv_heads, 2, D] as cache_append_ keeps it."""
+    if not isinstance(k_bounds, torch.Tensor) or k_bounds.dim() != 4:
+        raise ValueError("k_bounds must be a [num_pages, kv_heads, 2, D] tensor")
+    num_pages, heads, _, D = k_bounds.shape
+    code, dtype = (E4M3, torch.bfloat16) if k_bounds.dtype == torch.uint8 else (_dtype_code(k_bounds), k_bounds.dtype)
+    _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_bounds.dtype)
+    R, max_pages = _batch(block_table, lens, k_bounds)
+    Hq = _query(q, dtype, R, heads, D, k_bounds)
+    if budget < 1 or keep_first < 0 or budget <= keep_first:
+        raise ValueError(f"budget ({budget}) must be above keep_first ({keep_first}), and keep_first not negative")
+    _here(q, "q")
+    with _on(stream):
+        pages = torch.empty((R, heads, budget), dtype=torch.int32, device=q.device)
+        _check(lib.cpattn_select_pages(_p(q), _p(k_bounds), _p(block_table), _p(lens), _p(pages), R, Hq, heads, D,
+                                       page_size, max_pages, num_pages, budget, keep_first,
+                                       BF16 if dtype == torch.bfloat16 else FP32, code, _stream(stream)),
+               "cpattn_select_pages")
+    return pages
+
+
+def decode_workspace_bytes(R, Hq, Hkv, D) -> int:
+    return int(lib.cpattn_decode_workspace_bytes(R, Hq, Hkv, D))
+
+
+def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, scale=None, out_dtype=None, out=None,
+           lse=None, workspace=None, stream=None):
+    """Attention of one new token per request over a paged cache: (o [R, Hq, D] like
+    q, or of out_dtype; lse fp32 [R, Hq]).  pages: int32 [R, kv_heads, budget] as
+    select_pages gives them, or None for every page."""
+    (num_pages, heads, page_size, D), dtype, code = _cache(k_cache, kv_amax)
+    _expect(k_cache, "k_cache", k_cache.shape, k_cache.dtype)
+    _expect(v_cache, "v_cache", k_cache.shape, k_cache.dtype, k_cache)
+    R, max_pages = _batch(block_table, lens, k_cache)
+    Hq = _query(q, dtype, R, heads, D, k_cache)
+    budget = 0
+    if pages is not None:
+        if not isinstance(pages, torch.Tensor) or pages.dim() != 3:
+            raise ValueError("pages must be a [R, kv_heads, budget] tensor")
+        budget = pages.shape[2]
+        _expect(pages, "pages", (R, heads, budget), torch.int32, k_cache)
+    out_dtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    if out is not None:
+        _expect(out, "out", q.shape, out_dtype, k_cache)
+    if lse is not None:
+        _expect(lse, "lse", (R, Hq), torch.float32, k_cache)
+    scale = float(scale if scale is not None else D ** -0.5)
+    _here(q, "q")
+    with _on(stream):
+        o = torch.empty((R, Hq, D), dtype=out_dtype, device=q.device) if out is None else out
+        lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+        workspace = _workspace(workspace, decode_workspace_bytes(R, Hq, heads, D), q)
+        _check(lib.cpattn_decode(_p(q), _p(k_cache), _p(v_cache), _p(block_table), _p(lens), _p(pages), _p(o), _p(lse),
+                                 R, Hq, heads, D, page_size, max_pages, num_pages, budget, scale, _p(kv_amax),
+                                 _p(workspace), workspace.numel() * workspace.element_size(),
+                                 BF16 if dtype == torch.bfloat16 else FP32, code,
+                                 BF16 if out_dtype == torch.bfloat16 else FP32, _stream(stream)), "cpattn_decode")
+    return o, lse
+
+
 def sync_status(stream=None) -> int:
     return int(lib.cpattn_sync_status(_stream(stream)))
 
@@ -496,7 +694,8 @@ def debug_stall(n: int) -> int:
 KERNEL_KINDS = {0: "tc_fwd", 1: "simt_fwd", 2: "merge", 3: "finalize", 4: "bwd_delta",
                 5: "simt_dkdv", 6: "simt_dq", 7: "tc_dkdv", 8: "tc_dq", 9: "layer_heads",
                 10: "layer_colsum", 11: "accumulate", 12: "gemm", 13: "tc_fwd_fp8",
-                14: "quant_e4m3"}
+                14: "quant_e4m3", 15: "decode", 16: "decode_join", 17: "cache_plan",
+                18: "cache_append", 19: "select_pages"}
 
 
 def profile(on: bool) -> int:

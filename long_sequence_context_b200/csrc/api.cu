@@ -11,11 +11,13 @@
 
 #include "cpattn.h"
 #include "kernels.h"
+#include "paged.cuh"
 
 using namespace cpattn;
 
-// Error word written by kernels whose bounded waits ran out (one per device;
-// every device that loads the library holds its own copy of this variable).
+// Error word written by kernels whose bounded waits ran out or whose page
+// numbers are out of range (one per device; every device that loads the
+// library holds its own copy of this variable).
 __device__ unsigned int g_cpattn_error = 0;
 
 namespace {
@@ -119,6 +121,7 @@ const char* cpattn_status_str(int s) {
     case CPATTN_ERR_CUDA: return "CUDA error";
     case CPATTN_ERR_TIMEOUT: return "in-kernel wait timed out";
     case CPATTN_ERR_WORKSPACE: return "workspace missing or too small";
+    case CPATTN_ERR_PAGE: return "page, slot or length outside of the cache";
     default: return "unknown status";
   }
 }
@@ -309,7 +312,7 @@ int cpattn_sync_status(void* stream) {
     unsigned zero = 0;
     if (cudaMemcpyToSymbol(g_cpattn_error, &zero, sizeof(zero)) != cudaSuccess)
       return CPATTN_ERR_CUDA;
-    return CPATTN_ERR_TIMEOUT;
+    return (h & ~paged::kErrPage) ? CPATTN_ERR_TIMEOUT : CPATTN_ERR_PAGE;
   }
   return CPATTN_OK;
 }

@@ -116,7 +116,12 @@ enum KernelId : int {
   kKGemm = 12,        // projection GEMMs of the attention layer (cpattn_gemm)
   kKTcFwdFp8 = 13,    // tcgen05 forward on e4m3 inputs (cpattn_fwd_fp8)
   kKQuant = 14,       // max|x| and e4m3 quantisation (cpattn_amax, cpattn_quantize_e4m3)
-  kKNumKernels = 15
+  kKDecode = 15,      // single-token attention over the paged cache (cpattn_decode)
+  kKDecodeJoin = 16,  // the join of its partial results
+  kKCachePlan = 17,   // page and slot planning (cpattn_cache_plan)
+  kKCacheAppend = 18, // new rows into the paged cache (cpattn_cache_append)
+  kKSelect = 19,      // page scores and selection (cpattn_select_pages)
+  kKNumKernels = 20
 };
 void prof_begin(int kernel_id, cudaStream_t stream);
 void prof_end(int kernel_id, cudaStream_t stream);

@@ -1,0 +1,90 @@
+// paged.cuh -- what the paged key-value cache's translation units share: the
+// cache element types, the error bit of a page outside of the pool and small
+// conversions.
+//
+// Layout of a cache: [num_pages][Hkv][page_size][D], K and V apart, so that the
+// rows of one (page, kv head) are one contiguous block.  page_size is a power
+// of two from 16 to 256: 16 consecutive keys never straddle two pages.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+namespace cpattn {
+namespace paged {
+
+// bit of the device error word: a page number, slot or length out of range
+constexpr unsigned kErrPage = 4u;
+
+// An element of an 8-bit cache: the e4m3 code of x * s, s = 448 / max|x|.
+struct E4m3 {
+  uint8_t code;
+};
+
+constexpr int kMinPage = 16;
+constexpr int kMaxPage = 256;
+
+inline int page_shift(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == (1 << s)) return s;
+  return -1;
+}
+
+inline bool aligned_to(const void* p, unsigned n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+__device__ __forceinline__ float e4m3_scale(const float* amax) {
+  const float a = *amax;
+  return a > 0.f ? __fdiv_rn(448.f, a) : 1.f;
+}
+
+// two e4m3 codes (low byte first) as half precision, which holds every code exactly
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// N consecutive stored elements (4 * N / 4 ... bytes already in registers) as floats
+template <typename CT>
+struct Unpack;
+template <>
+struct Unpack<float> {
+  static constexpr int kPerWord = 1;
+  __device__ static __forceinline__ void word(uint32_t w, float* f) { f[0] = __uint_as_float(w); }
+};
+template <>
+struct Unpack<__nv_bfloat16> {
+  static constexpr int kPerWord = 2;
+  __device__ static __forceinline__ void word(uint32_t w, float* f) {
+    f[0] = __uint_as_float(w << 16);
+    f[1] = __uint_as_float(w & 0xffff0000u);
+  }
+};
+template <>
+struct Unpack<E4m3> {
+  static constexpr int kPerWord = 4;
+  __device__ static __forceinline__ void word(uint32_t w, float* f) {
+    const uint32_t a = e4m3x2_to_half2((uint16_t)(w & 0xffffu)), b = e4m3x2_to_half2((uint16_t)(w >> 16));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    f[0] = x.x;
+    f[1] = x.y;
+    f[2] = y.x;
+    f[3] = y.y;
+  }
+};
+
+}  // namespace paged
+}  // namespace cpattn
