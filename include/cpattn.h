@@ -336,8 +336,10 @@ int cpattn_gemm(const void* A, const void* B, const void* bias, void* C, int M, 
  *   k_bounds          [num_pages][Hkv][2][D] of cache_dtype: elementwise smallest
  *                     (row 0) and largest (row 1) key of each page, as stored
  *   kv_amax           device float[2], max|k| and max|v| that an e4m3 cache is
- *                     scaled by: code = e4m3(fp32(x * s)), s = 448 / amax, saturating
- *                     (as cpattn_quantize_e4m3); NULL for the other types
+ *                     scaled by: code = e4m3(fp32(x * s)), saturating, with s =
+ *                     448 * (1 / amax), both rounded to fp32 (448.0 / amax of a
+ *                     PyTorch tensor; the last bit may differ from the one-step
+ *                     quotient of cpattn_quantize_e4m3); NULL for the other types
  *   lens              [R] int32: tokens of request r that the cache holds
  *   block_table       [R][max_pages] int32: the page of tokens j * page_size ..
  *                     is block_table[r][j]; entries behind the last held page are

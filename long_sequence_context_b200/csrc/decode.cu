@@ -38,7 +38,7 @@ struct DecodeArgs {
   unsigned* err;
   int R, Hq, Hkv, group, shift, max_pages, num_pages, budget;
   float scale_log2;
-  int o_bf16, q_bf16;
+  int o_bf16;
 };
 
 // Keys of request r in the order its page list gives them (whole pages where
@@ -68,54 +68,59 @@ __device__ __forceinline__ void store_o(const DecodeArgs& a, size_t i, float x) 
     static_cast<float*>(a.o)[i] = x;
 }
 
-// One warp's view of 16 keys, in fp32 arithmetic.  Lane 4g + t holds, for
-// every 8 heads, the scores of keys g and g + 8 with heads 2t and 2t + 1, and
-// of the output the 8 columns 64h + 8g .. + 7 of the same two heads.
-template <typename CT, int D, int NT>
+// One warp's view of 16 keys.  Lane 4g + t holds, for every 8 heads, the scores
+// of keys g and g + 8 with heads 2t and 2t + 1, and of the output 8 columns for
+// every 64 (col()) of the same two heads: the accumulator layout of mma.m16n8k16
+// with the keys (scores) or the columns (output) as its 16 rows.
+//
+// FmaTile: fp32 caches, fp32 arithmetic throughout.
+template <int D, int NT>
 struct FmaTile {
-  static constexpr int kEpv = 16 / sizeof(CT);      // elements of a 16-byte load
-  static constexpr int kVecs = D / (4 * kEpv);      // loads of a lane's quarter of a row
-  static constexpr int kWpv = 8 * sizeof(CT) / 4;   // words of 8 elements
+  using CT = float;
+  static constexpr int kQueryBytes = D * 4;  // shared memory of one head's query
+  static constexpr float kLift = 0.f, kSlack = 8.f;
+  static constexpr int kCtas = NT == 1 ? 3 : 2;  // blocks of an SM
+  static constexpr int kVecs = D / 16;  // 16-byte loads of a lane's quarter of a row
 
-  // qs: the heads of this warp, [8 * NT][D] fp32
-  __device__ static __forceinline__ void scores(const CT* k, const float* qs, float (&s)[NT][4]) {
+  float4 k[2][kVecs];
+  const float* v_rows;
+
+  __device__ static __forceinline__ int col(int h, int g, int e) { return 64 * h + 8 * g + e; }
+
+  // the queries of `heads` heads from row `at` of q on, for all tiles of this block
+  __device__ static __forceinline__ void stage_queries(char* s, float*, const void* q, size_t at, int group, int heads) {
+    for (int i = threadIdx.x; i < heads * D; i += kThreads)
+      reinterpret_cast<float*>(s)[i] = i / D < group ? static_cast<const float*>(q)[at * D + i] : 0.f;
+  }
+
+  __device__ __forceinline__ void load_k(const CT* p) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint4 w[2][kVecs];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int j = 0; j < kVecs; ++j)
-        w[r][j] = __ldg(reinterpret_cast<const uint4*>(k + (g + 8 * r) * D + (j * 4 + t) * kEpv));
+        k[r][j] = __ldg(reinterpret_cast<const float4*>(p + (g + 8 * r) * D + (j * 4 + t) * 4));
+  }
+  __device__ __forceinline__ void load_v(const CT* p) { v_rows = p; }
+
+  __device__ __forceinline__ void scores(const char* s_q, float (&s)[NT][4]) const {
+    const int t = threadIdx.x & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float acc[2][8] = {};
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        float x[2][kEpv];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          constexpr int P = Unpack<CT>::kPerWord;
-          Unpack<CT>::word(w[r][j].x, x[r]);
-          Unpack<CT>::word(w[r][j].y, x[r] + P);
-          Unpack<CT>::word(w[r][j].z, x[r] + 2 * P);
-          Unpack<CT>::word(w[r][j].w, x[r] + 3 * P);
-        }
+      for (int j = 0; j < kVecs; ++j)
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          const float* q = qs + (nt * 8 + n) * D + (j * 4 + t) * kEpv;
+          const float4 f = *reinterpret_cast<const float4*>(s_q + (size_t)(nt * 8 + n) * D * 4 + (j * 4 + t) * 16);
 #pragma unroll
-          for (int e = 0; e < kEpv; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(q + e);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              acc[r][n] = fmaf(f.x, x[r][e], acc[r][n]);
-              acc[r][n] = fmaf(f.y, x[r][e + 1], acc[r][n]);
-              acc[r][n] = fmaf(f.z, x[r][e + 2], acc[r][n]);
-              acc[r][n] = fmaf(f.w, x[r][e + 3], acc[r][n]);
-            }
+          for (int r = 0; r < 2; ++r) {
+            acc[r][n] = fmaf(f.x, k[r][j].x, acc[r][n]);
+            acc[r][n] = fmaf(f.y, k[r][j].y, acc[r][n]);
+            acc[r][n] = fmaf(f.z, k[r][j].z, acc[r][n]);
+            acc[r][n] = fmaf(f.w, k[r][j].w, acc[r][n]);
           }
         }
-      }
       // sum over the quad; lane t is left with heads 2t and 2t + 1
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -135,32 +140,19 @@ struct FmaTile {
   }
 
   // acc += p v; n_valid: rows behind it hold anything and count as zero
-  __device__ static __forceinline__ void output(const CT* v, const float (&p)[NT][4], int n_valid,
-                                                float (&acc)[NT][D / 64][16]) {
+  __device__ __forceinline__ void output(const float (&p)[NT][4], int n_valid, float (&acc)[NT][D / 64][16]) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int kk = 0; kk < kChunk; ++kk) {
       float x[D / 64][8];
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(v + kk * D + 64 * h + 8 * g);
-        uint32_t w[kWpv];
-        if constexpr (kWpv == 2) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-          w[0] = u.x, w[1] = u.y;
-        } else {
+      for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-          for (int i = 0; i < kWpv; i += 4) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + i));
-            w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
-          }
+        for (int e = 0; e < 8; e += 4) {
+          float4 u = __ldg(reinterpret_cast<const float4*>(v_rows + kk * D + 64 * h + 8 * g + e));
+          if (kk >= n_valid) u = make_float4(0.f, 0.f, 0.f, 0.f);
+          x[h][e] = u.x, x[h][e + 1] = u.y, x[h][e + 2] = u.z, x[h][e + 3] = u.w;
         }
-#pragma unroll
-        for (int i = 0; i < kWpv; ++i) Unpack<CT>::word(w[i], x[h] + i * Unpack<CT>::kPerWord);
-        if (kk >= n_valid)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[h][e] = 0.f;
-      }
       const int src_lane = (kk & 7) * 4 + t;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -178,10 +170,229 @@ struct FmaTile {
   }
 };
 
-template <typename CT, int D, int NT>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
-  constexpr int HT = 8 * NT;  // heads of one warp
-  __shared__ float s_buf[kWarps * HT][D];  // the queries; then the warps' outputs
+__device__ __forceinline__ void mma_16816(bool half, float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  if (half)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// MmaTile: bf16 and e4m3 caches on the tensor cores, S^T = K Q^T and O^T = V^T P^T
+// with up to 8 heads as the narrow side, so that a group of few heads wastes
+// little.  K and V go from global memory straight into the operand registers:
+// the contraction index of a product and the row index of O^T may be permuted
+// at will, so a lane's 16-byte load of consecutive columns is at once its share
+// of one or more operands, and no shared memory, no wait and no barrier stands
+// between memory and the tensor cores.  8-bit codes are widened to half
+// precision, which holds them exactly; the queries then are in half precision
+// too, scaled per head by a power of two so that none of their bits is lost.
+// The weights enter as the sum of two 16-bit numbers (2^-17 relative or
+// better): the kernel waits for memory, the second product is free, and fp32
+// outputs stay good to that.
+template <typename C, int D, int NT>
+struct MmaTile {
+  using CT = C;
+  static constexpr bool kHalf = sizeof(C) == 1;
+  static constexpr int kQueryBytes = D * 2;
+  static constexpr int kCtas = NT == 1 ? 4 : 3;
+  // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
+  // ends at 2^-24, which must be far below the largest weight of a long context.
+  static constexpr float kLift = kHalf ? 14.f : 0.f, kSlack = kHalf ? 1.f : 8.f;
+  static constexpr int kRowVecs = D * (int)sizeof(C) / 64;  // 16-byte loads of a lane's quarter of a key
+  static constexpr int kVWords = D * (int)sizeof(C) / 32;   // words of a lane's eighth of a value row
+
+  uint32_t k[2][kRowVecs * 4];
+  uint32_t v[4][kVWords];
+
+  __device__ static __forceinline__ int col(int h, int g, int e) {
+    return kHalf ? D / 8 * g + 8 * h + e : 64 * h + 8 * g + e;
+  }
+  // the 8 columns that lane t's part of query entry e stands for
+  __device__ static __forceinline__ int query_col(int e, int t) {
+    return kHalf ? 64 * (e >> 1) + 16 * t + 8 * (e & 1) : 32 * e + 8 * t;
+  }
+
+  // s: [head / 8][entry][lane] 16 bytes, lane 4 * (head % 8) + t; unit[head]: what a score is multiplied by
+  __device__ static __forceinline__ void stage_queries(char* s, float* unit, const void* q, size_t at, int group, int heads) {
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(q) + at * D;
+    const int t = threadIdx.x & 3;
+    for (int head = threadIdx.x >> 2; head < heads; head += kThreads / 4) {  // a quad per head
+      uint4 w[D / 32];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        w[e] = head < group ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)head * D + query_col(e, t)))
+                            : make_uint4(0, 0, 0, 0);
+      if constexpr (kHalf) {
+        float f[D / 32][8], m = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) Unpack<__nv_bfloat16>::word(u[i], &f[e][2 * i]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[e][i]));
+        }
+        const unsigned quad = 0xfu << (threadIdx.x & 28);
+        m = fmaxf(m, __shfl_xor_sync(quad, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(quad, m, 2));
+        // 2^up m in [2^14, 2^15)
+        const int up = m > 0.f && m < INFINITY ? 14 - ilogbf(m) : 0;
+        if (t == 0) unit[head] = ldexpf(1.f, -up);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          uint32_t u[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 x = __floats2half2_rn(ldexpf(f[e][2 * i], up), ldexpf(f[e][2 * i + 1], up));
+            u[i] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          w[e] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      } else if (t == 0) {
+        unit[head] = 1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        reinterpret_cast<uint4*>(s)[((head >> 3) * (D / 32) + e) * 32 + (head & 7) * 4 + t] = w[e];
+    }
+  }
+
+  __device__ __forceinline__ void load_k(const CT* p) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < kRowVecs; ++j) {
+        const char* at = reinterpret_cast<const char*>(p) + (size_t)(g + 8 * r) * D * sizeof(CT) + j * 64 + t * 16;
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(at));
+        k[r][4 * j] = u.x, k[r][4 * j + 1] = u.y, k[r][4 * j + 2] = u.z, k[r][4 * j + 3] = u.w;
+      }
+  }
+  __device__ __forceinline__ void load_v(const CT* p) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = 2 * t + (i & 1) + 8 * (i >> 1);
+      const char* row = reinterpret_cast<const char*>(p) + (size_t)key * D * sizeof(CT);
+      if constexpr (kVWords == 2) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + g * 8));
+        v[i][0] = u.x, v[i][1] = u.y;
+      } else {
+#pragma unroll
+        for (int h = 0; h < kVWords / 4; ++h) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + h * 128 + g * 16));
+          v[i][4 * h] = u.x, v[i][4 * h + 1] = u.y, v[i][4 * h + 2] = u.z, v[i][4 * h + 3] = u.w;
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void scores(const char* s_q, float (&s)[NT][4]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      uint32_t a[2][4];  // rows g, g + 8: the operands of two steps of 16 columns
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if constexpr (kHalf) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            a[r][2 * i] = e4m3x2_to_half2((uint16_t)(k[r][2 * e + i] & 0xffffu));
+            a[r][2 * i + 1] = e4m3x2_to_half2((uint16_t)(k[r][2 * e + i] >> 16));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[r][i] = k[r][4 * e + i];
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 b = reinterpret_cast<const uint4*>(s_q)[(nt * (D / 32) + e) * 32 + lane];
+        mma_16816(kHalf, s[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+        mma_16816(kHalf, s[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+      }
+    }
+  }
+
+  __device__ __forceinline__ static uint32_t pack(float x, float y) {
+    if constexpr (kHalf) {
+      const __half2 h = __floats2half2_rn(x, y);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  __device__ __forceinline__ static float2 unpack(uint32_t w) {
+    if constexpr (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+
+  __device__ __forceinline__ void output(const float (&p)[NT][4], int n_valid, float (&acc)[NT][D / 64][16]) {
+    const int t = threadIdx.x & 3;
+    if (n_valid < kChunk) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (2 * t + (i & 1) + 8 * (i >> 1) >= n_valid)
+#pragma unroll
+          for (int w = 0; w < kVWords; ++w) v[i][w] = 0u;
+    }
+    uint32_t b[NT][2][2];  // [head tile][high, low part][keys 0-7, 8-15]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t hi = pack(p[nt][2 * r], p[nt][2 * r + 1]);
+        const float2 f = unpack(hi);
+        b[nt][0][r] = transpose8x8(hi);
+        b[nt][1][r] = transpose8x8(pack(p[nt][2 * r] - f.x, p[nt][2 * r + 1] - f.y));
+      }
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        uint32_t w[4];  // columns col(h, g, 2m), + 1 of the lane's four keys
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kHalf) {
+            const uint32_t x = v[i][2 * h + (m >> 1)];
+            w[i] = e4m3x2_to_half2((uint16_t)((m & 1) ? x >> 16 : x & 0xffffu));
+          } else {
+            w[i] = v[i][4 * h + m];
+          }
+        }
+        const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
+        const uint32_t a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816(kHalf, &acc[nt][h][4 * m], a0, a1, a2, a3, b[nt][0][0], b[nt][0][1]);
+          mma_16816(kHalf, &acc[nt][h][4 * m], a0, a1, a2, a3, b[nt][1][0], b[nt][1][1]);
+        }
+      }
+  }
+};
+
+template <typename Tile, int D, int NT>
+__global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const DecodeArgs a) {
+  using CT = typename Tile::CT;
+  constexpr int HT = 8 * NT;                           // heads of one warp
+  __shared__ __align__(16) float s_buf[kWarps * HT][D];  // the queries; then the warps' outputs
+  __shared__ float s_unit[kWarps * HT];
   __shared__ float s_m[kWarps][HT], s_l[kWarps][HT];
   __shared__ long long s_scan[kWarps], s_base;
   __shared__ int s_r;
@@ -260,16 +471,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
     const int32_t* list = a.pages ? a.pages + ((size_t)r * a.Hkv + h) * a.budget : nullptr;
 
     __syncthreads();  // the previous pair's queries and partial outputs are read
-    for (int i = tid; i < hgroups * HT * D; i += kThreads) {
-      const int head = i / D;
-      float x = 0.f;
-      if (head < a.group) {
-        const size_t at = ((size_t)r * a.Hq + (size_t)h * a.group + head) * D + i % D;
-        x = a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at])
-                     : static_cast<const float*>(a.q)[at];
-      }
-      s_buf[head][i % D] = x;
-    }
+    Tile::stage_queries(reinterpret_cast<char*>(s_buf), s_unit, a.q, (size_t)r * a.Hq + (size_t)h * a.group, a.group,
+                        hgroups * HT);
     __syncthreads();
 
     float m[NT][2], l[NT][2], acc[NT][D / 64][16];
@@ -283,52 +486,86 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
         for (int e = 0; e < 16; ++e) acc[nt][hh][e] = 0.f;
     }
 
-    for (int c = x0 * 4 + kw; c < x1 * 4; c += kwarps) {
+    const char* s_q = reinterpret_cast<const char*>(s_buf) + hg * HT * Tile::kQueryBytes;
+    float unit[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        unit[nt][i] = scale_log2 * (sizeof(CT) == 1 ? s_unit[hg * HT + nt * 8 + 2 * t + i] : 1.f);
+
+    // Chunk c of the pair: its first row in the cache and how many of its 16 keys
+    // count; chunks that are not there read row 0 and count none.
+    auto locate = [&](int c, int& n_valid) -> size_t {
+      n_valid = 0;
       const int j = (int)(((long long)c * kChunk) >> a.shift);
-      if (j >= n_list) break;
+      if (c >= x1 * 4 || j >= n_list) return 0;
       const int off = (c * kChunk) & ((1 << a.shift) - 1);
       const int logical = list ? list[j] : j;
-      const long long pos = ((long long)logical << a.shift) + off;  // of the chunk's first key
-      if (logical < 0 || pos >= len) continue;                        // padding of the list, or the end
+      const long long pos = ((long long)logical << a.shift) + off;
+      if (logical < 0 || pos >= len) return 0;  // padding of the list, or behind the end
       const int page = table[logical];
       if (page < 0 || page >= a.num_pages) {
         if (lane == 0) atomicOr(a.err, kErrPage);
-        continue;
+        return 0;
       }
-      const int n_valid = (int)min((long long)kChunk, len - pos);
-      const size_t row = ((((size_t)page * a.Hkv + h) << a.shift) + off) * D;
-      const CT* k = static_cast<const CT*>(a.k) + row;
-      const CT* v = static_cast<const CT*>(a.v) + row;
+      n_valid = (int)min((long long)kChunk, len - pos);
+      return ((((size_t)page * a.Hkv + h) << a.shift) + off) * D;
+    };
 
+    // K of the next chunk is on its way while this one's softmax and output run;
+    // where it stands is known one chunk earlier still.
+    Tile tile;
+    const CT* kc = static_cast<const CT*>(a.k);
+    const CT* vc = static_cast<const CT*>(a.v);
+    int c = x0 * 4 + kw, n_valid, n_next;
+    size_t row = locate(c, n_valid), row_next = locate(c + kwarps, n_next);
+    if (c < x1 * 4) tile.load_k(kc + row);
+    for (; c < x1 * 4; c += kwarps) {
+      tile.load_v(vc + row);
+      int n_after;
+      const size_t row_after = locate(c + 2 * kwarps, n_after);
       float s[NT][4];
-      FmaTile<CT, D, NT>::scores(k, s_buf[hg * HT], s);
+      tile.scores(s_q, s);
+      if (c + kwarps < x1 * 4) tile.load_k(kc + row_next);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = (g + 8 * (i >> 1)) < n_valid ? s[nt][i] * scale_log2 : -INFINITY;
-        float base2[2];
+        for (int i = 0; i < 4; ++i) s[nt][i] = (g + 8 * (i >> 1)) < n_valid ? s[nt][i] * unit[nt][i & 1] : -INFINITY;
+        float mx[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = fmaxf(s[nt][i], s[nt][i + 2]);
+          mx[i] = fmaxf(s[nt][i], s[nt][i + 2]);
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          mx = fmaxf(mx, m[nt][i]);
-          base2[i] = mx == -INFINITY ? 0.f : mx;
-          const float alpha = exp2f(m[nt][i] - base2[i]);
-          m[nt][i] = mx;
-          l[nt][i] *= alpha;
+          for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+        }
+        // the reference of the weights follows the maximum only when that has grown by kSlack
+        if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + (Tile::kLift + Tile::kSlack) ||
+                                        mx[1] > m[nt][1] + (Tile::kLift + Tile::kSlack))) {
 #pragma unroll
-          for (int hh = 0; hh < D / 64; ++hh)
+          for (int i = 0; i < 2; ++i) {
+            const float mn = fmaxf(m[nt][i], mx[i] - Tile::kLift);
+            const float alpha = exp2f(m[nt][i] - (mn == -INFINITY ? 0.f : mn));
+            m[nt][i] = mn;
+            l[nt][i] *= alpha;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[nt][hh][2 * e + i] *= alpha;
+            for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[nt][hh][2 * e + i] *= alpha;
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[nt][i] = exp2f(s[nt][i] - base2[i & 1]);
+          const float b = m[nt][i & 1];
+          s[nt][i] = exp2f(s[nt][i] - (b == -INFINITY ? 0.f : b));
           l[nt][i & 1] += s[nt][i];
         }
       }
-      FmaTile<CT, D, NT>::output(v, s, n_valid, acc);
+      tile.output(s, n_valid, acc);
+      row = row_next;
+      n_valid = n_next;
+      row_next = row_after;
+      n_next = n_after;
     }
 
     // the warps' results side by side, then one per head
@@ -344,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
 #pragma unroll
         for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s_buf[warp * HT + head][64 * hh + 8 * g + e] = acc[nt][hh][2 * e + i];
+          for (int e = 0; e < 8; ++e) s_buf[warp * HT + head][Tile::col(hh, g, e)] = acc[nt][hh][2 * e + i];
       }
     __syncthreads();
     const bool whole = x0 == 0 && x1 == n_units;
@@ -437,29 +674,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs 
   }
 }
 
-constexpr int kCtasPerSm = 3;
-
-int decode_grid(long long max_units) {
+int decode_grid(int ctas, long long max_units) {
   int dev = 0;
   cudaGetDevice(&dev);
-  return (int)std::min<long long>((long long)num_sms(dev) * kCtasPerSm, std::max<long long>(1, max_units));
+  return (int)std::min<long long>((long long)num_sms(dev) * ctas, std::max<long long>(1, max_units));
 }
 
-template <typename CT, int D>
-void launch_nt(const DecodeArgs& a, int grid, cudaStream_t s) {
-  if (a.group <= 8)
-    decode_kernel<CT, D, 1><<<grid, kThreads, 0, s>>>(a);
-  else
-    decode_kernel<CT, D, 2><<<grid, kThreads, 0, s>>>(a);
+bool sizes_ok(int R, int Hq, int Hkv, int D) {
+  if (R < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kMaxGroup) return false;
+  return D == 64 || D == 128;
 }
 
-template <typename CT>
-int launch_decode(const DecodeArgs& a, int D, int grid, cudaStream_t s) {
+// bytes of the workspace of a grid: partial outputs, (maximum, sum) pairs, tails
+size_t ws_part_o(int grid, int group, int D) { return (size_t)2 * grid * group * D * sizeof(float); }
+size_t ws_part_ml(int grid, int group) { return ((size_t)2 * grid * group * 2 * sizeof(float) + 15) & ~(size_t)15; }
+constexpr int kMostCtas = 4;  // blocks of an SM, over all variants
+
+template <typename Tile, int D, int NT>
+int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
+  static_assert(Tile::kCtas <= kMostCtas, "the workspace is sized for kMostCtas");
+  const int grid = decode_grid(Tile::kCtas, max_units);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float*>(ws + ws_part_o(grid, a.group, D));
+  a.tail = reinterpret_cast<int4*>(ws + ws_part_o(grid, a.group, D) + ws_part_ml(grid, a.group));
   prof_begin(kKDecode, s);
-  if (D == 64)
-    launch_nt<CT, 64>(a, grid, s);
-  else
-    launch_nt<CT, 128>(a, grid, s);
+  decode_kernel<Tile, D, NT><<<grid, kThreads, 0, s>>>(a);
   prof_end(kKDecode, s);
   if (cudaGetLastError() != cudaSuccess) return -1;
   // the join starts while the last blocks finish and waits for them on the device
@@ -473,19 +712,26 @@ int launch_decode(const DecodeArgs& a, int D, int grid, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   prof_begin(kKDecodeJoin, s);
-  const cudaError_t e = D == 64 ? cudaLaunchKernelEx(&cfg, join_kernel<64>, a) : cudaLaunchKernelEx(&cfg, join_kernel<128>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<D>, a);
   prof_end(kKDecodeJoin, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 2 : -1;
 }
 
-bool sizes_ok(int R, int Hq, int Hkv, int D) {
-  if (R < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kMaxGroup) return false;
-  return D == 64 || D == 128;
+template <int D>
+int launch_decode(const DecodeArgs& a, int cache_dtype, cudaStream_t s, long long max_units, char* ws) {
+  const bool one = a.group <= 8;  // head tiles of a warp
+  switch (cache_dtype) {
+    case CPATTN_BF16:
+      return one ? launch_tile<MmaTile<__nv_bfloat16, D, 1>, D, 1>(a, s, max_units, ws)
+                 : launch_tile<MmaTile<__nv_bfloat16, D, 2>, D, 2>(a, s, max_units, ws);
+    case CPATTN_FP32:
+      return one ? launch_tile<FmaTile<D, 1>, D, 1>(a, s, max_units, ws)
+                 : launch_tile<FmaTile<D, 2>, D, 2>(a, s, max_units, ws);
+    default:
+      return one ? launch_tile<MmaTile<E4m3, D, 1>, D, 1>(a, s, max_units, ws)
+                 : launch_tile<MmaTile<E4m3, D, 2>, D, 2>(a, s, max_units, ws);
+  }
 }
-
-// bytes of the workspace of a grid: partial outputs, (maximum, sum) pairs, tails
-size_t ws_part_o(int grid, int group, int D) { return (size_t)2 * grid * group * D * sizeof(float); }
-size_t ws_part_ml(int grid, int group) { return ((size_t)2 * grid * group * 2 * sizeof(float) + 15) & ~(size_t)15; }
 
 }  // namespace
 }  // namespace cpattn
@@ -496,7 +742,7 @@ extern "C" {
 
 size_t cpattn_decode_workspace_bytes(int R, int Hq, int Hkv, int D) {
   if (!sizes_ok(R, Hq, Hkv, D)) return 0;
-  const int grid = decode_grid(1LL << 40), group = Hq / Hkv;
+  const int grid = decode_grid(kMostCtas, 1LL << 40), group = Hq / Hkv;
   return ws_part_o(grid, group, D) + ws_part_ml(grid, group) + (size_t)grid * sizeof(int4);
 }
 
@@ -547,18 +793,12 @@ int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,
   a.budget = budget;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o_bf16 = o_dtype == CPATTN_BF16;
-  a.q_bf16 = dtype == CPATTN_BF16;
   const long long listed = pages ? std::min(budget, max_pages) : max_pages;
-  const int grid = decode_grid((long long)R * Hkv * (((listed << shift) + kUnit - 1) / kUnit));
-  char* ws = static_cast<char*>(workspace);
-  a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float*>(ws + ws_part_o(grid, a.group, D));
-  a.tail = reinterpret_cast<int4*>(ws + ws_part_o(grid, a.group, D) + ws_part_ml(grid, a.group));
+  const long long max_units = (long long)R * Hkv * (((listed << shift) + kUnit - 1) / kUnit);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int n = -1;
-  if (cache_dtype == CPATTN_BF16) n = launch_decode<__nv_bfloat16>(a, D, grid, s);
-  else if (cache_dtype == CPATTN_FP32) n = launch_decode<float>(a, D, grid, s);
-  else n = launch_decode<paged::E4m3>(a, D, grid, s);
+  char* ws = static_cast<char*>(workspace);
+  const int n = D == 64 ? launch_decode<64>(a, cache_dtype, s, max_units, ws)
+                        : launch_decode<128>(a, cache_dtype, s, max_units, ws);
   if (n < 0) return CPATTN_ERR_CUDA;
   add_launches(n);
   return CPATTN_OK;

@@ -20,7 +20,7 @@ namespace paged {
 // bit of the device error word: a page number, slot or length out of range
 constexpr unsigned kErrPage = 4u;
 
-// An element of an 8-bit cache: the e4m3 code of x * s, s = 448 / max|x|.
+// An element of an 8-bit cache: the e4m3 code of x * s, s = 448 * (1 / max|x|).
 struct E4m3 {
   uint8_t code;
 };
@@ -38,9 +38,13 @@ inline bool aligned_to(const void* p, unsigned n) {
   return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+// 448 * (1 / amax), both steps rounded to fp32: what 448.0 / amax gives for a
+// tensor in PyTorch, so that codes a program writes with torch and codes written
+// here agree bit for bit.  (The one-step quotient of cpattn_quantize_e4m3 can
+// differ in the last bit.)
 __device__ __forceinline__ float e4m3_scale(const float* amax) {
   const float a = *amax;
-  return a > 0.f ? __fdiv_rn(448.f, a) : 1.f;
+  return a > 0.f ? __fmul_rn(__fdiv_rn(1.f, a), 448.f) : 1.f;
 }
 
 // two e4m3 codes (low byte first) as half precision, which holds every code exactly

@@ -7,20 +7,29 @@ from oracle import fp8, paged
 DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32, "e4m3": torch.uint8}
 
 
+def cache_scale(amax):
+    """448 * (1 / amax) in fp32, both steps rounded."""
+    return np.float32(448.0) * (np.float32(1.0) / np.float32(amax))
+
+
 def values(x, amax=None):
-    """fp64 values a stored tensor stands for (8-bit codes with the scale 448 / amax)."""
+    """fp64 values a stored tensor stands for (8-bit codes with cache_scale(amax))."""
     if x.dtype == torch.uint8:
-        s = np.float64(np.float32(448.0) / np.float32(amax)) if amax else 1.0
+        s = np.float64(cache_scale(amax)) if amax else 1.0
         return x.cpu().view(torch.float8_e4m3fn).float().numpy().astype(np.float64) / s
     return x.detach().float().cpu().numpy().astype(np.float64)
+
+
+def codes_of(x, amax):
+    """e4m3 codes (uint8 array) of rows x, by the oracle's encoder."""
+    return fp8.encode(x.float().numpy() * cache_scale(amax))
 
 
 def stored(x, kind, amax=None):
     """A CPU tensor of fp32 numbers as the cache stores it."""
     if kind != "e4m3":
         return x.to(DTYPES[kind])
-    codes, _, _ = fp8.quantize(x.to(torch.bfloat16).float().numpy(), np.float32(amax))
-    return torch.from_numpy(np.asarray(codes)).view(torch.uint8).reshape(x.shape)
+    return torch.from_numpy(codes_of(x.to(torch.bfloat16), amax))
 
 
 def rows_dtype(kind):

@@ -149,8 +149,8 @@ def test_decode_cache_offsets_beyond_32_bits(cp):
     slots = torch.tensor([(n - 1) * P + 5, (n - 1) * P + 6], device="cuda")
     cp.cache_append_(rows, rows, slots, k, k.clone(), kv_amax=c["amax"].cuda())
     assert cp.sync_status() == cp.OK
-    want = cp.quantize_e4m3(rows[None], c["amax"][:1].cuda())[0]
-    assert torch.equal(k[n - 1, :, 5:7].transpose(0, 1), want)
+    want = torch.from_numpy(pu.codes_of(rows.cpu(), a[0]))
+    assert torch.equal(k[n - 1, :, 5:7].transpose(0, 1).cpu(), want)
 
 
 # ---- selected pages ----
@@ -309,8 +309,7 @@ def test_append_matches_oracle_bit_for_bit(cp, kind, heads_first, Hkv, D, P):
         put = []
         for i, x in enumerate(rows):
             if kind == "e4m3":
-                codes, _, _ = fp8.quantize(x.float().numpy(), np.float32(amax[i]))
-                put.append(fp8.DECODE[codes.astype(np.int64)])
+                put.append(fp8.decode(pu.codes_of(x, amax[i].item())))
             else:
                 put.append(pu.values(x))
         shadow = tuple(paged.append(c, x, slots.tolist()) for c, x in zip(shadow, put))
