@@ -6,7 +6,6 @@ turns a non-zero status into an exception.  All arithmetic runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback.  If the shared
 library has not been built, importing this module raises.
 """
-import contextlib
 import ctypes
 import os
 
@@ -480,44 +479,51 @@ def layer_bwd(x, w_qkv, w_o, saved, dy, num_heads: int, cp_size: int, causal: bo
     return dx, dw_qkv, db_qkv, dw_o, db_o
 
 
-def _cache(k_cache, kv_amax):
-    """Checks a paged cache tensor; returns (sizes, rows' dtype, dtype code)."""
+# ---- the paged key-value cache ----
+#
+# One token's step is a handful of calls of some microseconds each, so these
+# checks are kept short: one comparison per tensor, and the message only for a
+# tensor that fails it.
+
+def _fits(t, shape, dtype, dev) -> bool:
+    return isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.get_device() == dev \
+        and t.is_contiguous()
+
+
+def _cache(k_cache, v_cache, kv_amax):
+    """Checks a paged cache; returns (its sizes, the rows' dtype, its dtype code, its device)."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [num_pages, kv_heads, page_size, D] tensor")
-    if k_cache.dtype == torch.uint8:
+    shape, dtype, dev = k_cache.shape, k_cache.dtype, k_cache.get_device()
+    code = E4M3 if dtype == torch.uint8 else _dtype_code(k_cache)
+    if 0 in shape:
+        raise ValueError(f"k_cache is empty: {tuple(shape)}")
+    if not k_cache.is_contiguous():
+        raise ValueError("k_cache must be contiguous")
+    if not _fits(v_cache, shape, dtype, dev):
+        _expect(v_cache, "v_cache", shape, dtype, k_cache)
+    if code == E4M3:
         if kv_amax is None:
             raise ValueError("kv_amax must be given for an e4m3 (uint8) cache")
-        _expect(kv_amax, "kv_amax", (2,), torch.float32, k_cache)
-        return k_cache.shape, torch.bfloat16, E4M3
+        if not _fits(kv_amax, (2,), torch.float32, dev):
+            _expect(kv_amax, "kv_amax", (2,), torch.float32, k_cache)
+        return shape, torch.bfloat16, code, dev
     if kv_amax is not None:
         raise ValueError("kv_amax is for an e4m3 (uint8) cache only")
-    return k_cache.shape, k_cache.dtype, _dtype_code(k_cache)
-
-
-def _here(t: torch.Tensor, name: str):
-    """The paged cache's kernels start on the current device: `t` must be there."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _on(stream):
-    """Outputs and workspaces of a call are allocated for the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
+    return shape, dtype, code, dev
 
 
 def _batch(block_table, lens, like=None):
-    """Checks a page table [R, max_pages] and the lengths [R]."""
+    """Checks a page table [R, max_pages] and the lengths [R]; returns (R, max_pages)."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a [R, max_pages] tensor")
-    _expect(block_table, "block_table", block_table.shape, torch.int32, like)
-    _expect(lens, "lens", block_table.shape[:1], torch.int32, block_table)
-    return block_table.shape
+    shape = block_table.shape
+    dev = (block_table if like is None else like).get_device()
+    if not _fits(block_table, shape, torch.int32, dev):
+        _expect(block_table, "block_table", shape, torch.int32, like)
+    if not _fits(lens, shape[:1], torch.int32, dev):
+        _expect(lens, "lens", shape[:1], torch.int32, block_table)
+    return shape
 
 
 def _query(q, dtype, R, heads, D, like):
@@ -525,10 +531,24 @@ def _query(q, dtype, R, heads, D, like):
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [R, Hq, D] tensor")
     Hq = q.shape[1]
-    _expect(q, "q", (R, Hq, D), dtype, like)
+    if not _fits(q, (R, Hq, D), dtype, like.get_device()):
+        _expect(q, "q", (R, Hq, D), dtype, like)
     if Hq % heads != 0:
         raise ValueError(f"q has {Hq} heads, not a multiple of the cache's {heads}")
     return Hq
+
+
+def _here(t, name: str, dev: int):
+    """The kernels start on the current device: `t` (on device `dev`) must be there."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def cache_plan_workspace_bytes(R) -> int:
@@ -544,62 +564,74 @@ def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, 
     lens and free_state themselves), the first new token of each request, the slot
     of each new token (`capacity` of them, -1 behind the last) and 0 or PLAN_* bits
     (then nothing changed)."""
+    if stream is not None:  # outputs and workspaces are allocated for the stream the call runs on
+        with torch.cuda.stream(stream):
+            return cache_plan(lens, delta, block_table, free_ring, free_state, page_size, capacity, lens_out,
+                              free_state_out, workspace)
     R, max_pages = _batch(block_table, lens)
-    _expect(delta, "delta", (R,), torch.int32, block_table)
+    dev = block_table.get_device()
+    if not _fits(delta, (R,), torch.int32, dev):
+        _expect(delta, "delta", (R,), torch.int32, block_table)
     if not isinstance(free_ring, torch.Tensor) or free_ring.dim() != 1:
         raise ValueError("free_ring must be a [num_pages] tensor")
-    _expect(free_ring, "free_ring", free_ring.shape, torch.int32, block_table)
-    _expect(free_state, "free_state", (2,), torch.int32, block_table)
+    num_pages = free_ring.shape[0]
+    if not _fits(free_ring, (num_pages,), torch.int32, dev):
+        _expect(free_ring, "free_ring", (num_pages,), torch.int32, block_table)
+    if not _fits(free_state, (2,), torch.int32, dev):
+        _expect(free_state, "free_state", (2,), torch.int32, block_table)
     if lens_out is not None:
         _expect(lens_out, "lens_out", (R,), torch.int32, block_table)
     if free_state_out is not None:
         _expect(free_state_out, "free_state_out", (2,), torch.int32, block_table)
-    _here(block_table, "block_table")
-    need = cache_plan_workspace_bytes(R)
-    with _on(stream):
-        i32 = dict(dtype=torch.int32, device=block_table.device)
-        lens_out = torch.empty(R, **i32) if lens_out is None else lens_out
-        free_state_out = torch.empty(2, **i32) if free_state_out is None else free_state_out
-        cu_new, verdict = torch.empty(R + 1, **i32), torch.empty(1, **i32)
-        slots = torch.empty(max(0, capacity), dtype=torch.int64, device=block_table.device)
-        workspace = _workspace(workspace, need, block_table)
-        _check(lib.cpattn_cache_plan(_p(lens), _p(delta), _p(block_table), R, max_pages, page_size, _p(free_ring),
-                                     _p(free_state), free_ring.shape[0], _p(lens_out), _p(free_state_out),
-                                     _p(cu_new), _p(slots), capacity, _p(verdict), _p(workspace),
-                                     workspace.numel() * workspace.element_size(), _stream(stream)),
-               "cpattn_cache_plan")
+    s = _here(block_table, "block_table", dev)
+    need = 4 * (2 * R + 8)  # cpattn_cache_plan_workspace_bytes(R), rounded up
+    lens_out = torch.empty_like(lens) if lens_out is None else lens_out
+    free_state_out = torch.empty_like(free_state) if free_state_out is None else free_state_out
+    cu_new, verdict = lens.new_empty(R + 1), lens.new_empty(1)
+    slots = torch.empty(max(0, capacity), dtype=torch.int64, device=block_table.device)
+    workspace = lens.new_empty(need // 4) if workspace is None else _workspace(workspace, need, block_table)
+    _check(lib.cpattn_cache_plan(lens.data_ptr(), delta.data_ptr(), block_table.data_ptr(), R, max_pages, page_size,
+                                 free_ring.data_ptr(), free_state.data_ptr(), num_pages, lens_out.data_ptr(),
+                                 free_state_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), capacity,
+                                 verdict.data_ptr(), workspace.data_ptr(), need, s), "cpattn_cache_plan")
     return lens_out, free_state_out, cu_new, slots, verdict
+
+
+def _rows(t, name, shape, dtype, like):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    return st
 
 
 def cache_append_(k_new, v_new, slots, k_cache, v_cache, k_bounds=None, kv_amax=None, stream=None):
     """New rows into a paged cache (in place): k_new, v_new [N, kv_heads, D] with
     contiguous columns (views of [kv_heads, N, D] too), slots [N] int64 (negative:
     skipped).  k_bounds [num_pages, kv_heads, 2, D] is kept up to date when given."""
-    (num_pages, heads, page_size, D), dtype, code = _cache(k_cache, kv_amax)
-    _expect(k_cache, "k_cache", k_cache.shape, k_cache.dtype)
-    _expect(v_cache, "v_cache", k_cache.shape, k_cache.dtype, k_cache)
-    if k_bounds is not None:
+    (num_pages, heads, page_size, D), dtype, code, dev = _cache(k_cache, v_cache, kv_amax)
+    if k_bounds is not None and not _fits(k_bounds, (num_pages, heads, 2, D), k_cache.dtype, dev):
         _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_cache.dtype, k_cache)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a [N] tensor")
     N = slots.shape[0]
-    _expect(slots, "slots", (N,), torch.int64, k_cache)
-    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a torch.Tensor")
-        if tuple(t.shape) != (N, heads, D):
-            raise ValueError(f"{n} must have shape {(N, heads, D)}, got {tuple(t.shape)}")
-        if t.dtype != dtype:
-            raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
-        if t.device != k_cache.device:
-            raise ValueError(f"{n} is on {t.device}, expected {k_cache.device}")
-        if t.stride(2) != 1:
-            raise ValueError(f"{n} must have contiguous columns")
-    _here(k_cache, "k_cache")
-    _check(lib.cpattn_cache_append(_p(k_new), _p(v_new), k_new.stride(0), k_new.stride(1), v_new.stride(0),
-                                   v_new.stride(1), _p(slots), N, _p(k_cache), _p(v_cache), _p(k_bounds), heads, D,
-                                   page_size, num_pages, _p(kv_amax), BF16 if dtype == torch.bfloat16 else FP32,
-                                   code, _stream(stream)), "cpattn_cache_append")
+    if not _fits(slots, (N,), torch.int64, dev):
+        _expect(slots, "slots", (N,), torch.int64, k_cache)
+    ks = _rows(k_new, "k_new", (N, heads, D), dtype, k_cache)
+    vs = _rows(v_new, "v_new", (N, heads, D), dtype, k_cache)
+    s = _here(k_cache, "k_cache", dev)
+    if stream is not None:
+        s = stream.cuda_stream
+    _check(lib.cpattn_cache_append(k_new.data_ptr(), v_new.data_ptr(), ks[0], ks[1], vs[0], vs[1], slots.data_ptr(), N,
+                                   k_cache.data_ptr(), v_cache.data_ptr(), _p(k_bounds), heads, D, page_size, num_pages,
+                                   _p(kv_amax), FP32 if dtype == torch.float32 else BF16, code, s), "cpattn_cache_append")
     return k_cache, v_cache
 
 
@@ -607,22 +639,27 @@ def select_pages(q, k_bounds, block_table, lens, page_size: int, budget: int, ke
     """The pages one new token per request attends to: int32 [R, kv_heads, budget],
     ascending, -1 behind the last (see cpattn_select_pages in include/cpattn.h).
     q [R, Hq, D]; k_bounds [num_pages, kv_heads, 2, D] as cache_append_ keeps it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return select_pages(q, k_bounds, block_table, lens, page_size, budget, keep_first)
     if not isinstance(k_bounds, torch.Tensor) or k_bounds.dim() != 4:
         raise ValueError("k_bounds must be a [num_pages, kv_heads, 2, D] tensor")
     num_pages, heads, _, D = k_bounds.shape
     code, dtype = (E4M3, torch.bfloat16) if k_bounds.dtype == torch.uint8 else (_dtype_code(k_bounds), k_bounds.dtype)
-    _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_bounds.dtype)
+    dev = k_bounds.get_device()
+    if 0 in k_bounds.shape:
+        raise ValueError(f"k_bounds is empty: {tuple(k_bounds.shape)}")
+    if not _fits(k_bounds, (num_pages, heads, 2, D), k_bounds.dtype, dev):
+        _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_bounds.dtype)
     R, max_pages = _batch(block_table, lens, k_bounds)
     Hq = _query(q, dtype, R, heads, D, k_bounds)
     if budget < 1 or keep_first < 0 or budget <= keep_first:
         raise ValueError(f"budget ({budget}) must be above keep_first ({keep_first}), and keep_first not negative")
-    _here(q, "q")
-    with _on(stream):
-        pages = torch.empty((R, heads, budget), dtype=torch.int32, device=q.device)
-        _check(lib.cpattn_select_pages(_p(q), _p(k_bounds), _p(block_table), _p(lens), _p(pages), R, Hq, heads, D,
-                                       page_size, max_pages, num_pages, budget, keep_first,
-                                       BF16 if dtype == torch.bfloat16 else FP32, code, _stream(stream)),
-               "cpattn_select_pages")
+    s = _here(q, "q", dev)
+    pages = torch.empty((R, heads, budget), dtype=torch.int32, device=q.device)
+    _check(lib.cpattn_select_pages(q.data_ptr(), k_bounds.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+                                   pages.data_ptr(), R, Hq, heads, D, page_size, max_pages, num_pages, budget, keep_first,
+                                   FP32 if dtype == torch.float32 else BF16, code, s), "cpattn_select_pages")
     return pages
 
 
@@ -630,14 +667,18 @@ def decode_workspace_bytes(R, Hq, Hkv, D) -> int:
     return int(lib.cpattn_decode_workspace_bytes(R, Hq, Hkv, D))
 
 
+_decode_need = {}  # (device, Hq, Hkv, D) -> workspace bytes
+
+
 def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, scale=None, out_dtype=None, out=None,
            lse=None, workspace=None, stream=None):
     """Attention of one new token per request over a paged cache: (o [R, Hq, D] like
     q, or of out_dtype; lse fp32 [R, Hq]).  pages: int32 [R, kv_heads, budget] as
     select_pages gives them, or None for every page."""
-    (num_pages, heads, page_size, D), dtype, code = _cache(k_cache, kv_amax)
-    _expect(k_cache, "k_cache", k_cache.shape, k_cache.dtype)
-    _expect(v_cache, "v_cache", k_cache.shape, k_cache.dtype, k_cache)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode(q, k_cache, v_cache, block_table, lens, pages, kv_amax, scale, out_dtype, out, lse, workspace)
+    (num_pages, heads, page_size, D), dtype, code, dev = _cache(k_cache, v_cache, kv_amax)
     R, max_pages = _batch(block_table, lens, k_cache)
     Hq = _query(q, dtype, R, heads, D, k_cache)
     budget = 0
@@ -645,25 +686,28 @@ def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, sca
         if not isinstance(pages, torch.Tensor) or pages.dim() != 3:
             raise ValueError("pages must be a [R, kv_heads, budget] tensor")
         budget = pages.shape[2]
-        _expect(pages, "pages", (R, heads, budget), torch.int32, k_cache)
+        if not _fits(pages, (R, heads, budget), torch.int32, dev):
+            _expect(pages, "pages", (R, heads, budget), torch.int32, k_cache)
     out_dtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype != torch.bfloat16 and out_dtype != torch.float32:
         raise TypeError(f"unsupported dtype {out_dtype}")
     if out is not None:
         _expect(out, "out", q.shape, out_dtype, k_cache)
     if lse is not None:
         _expect(lse, "lse", (R, Hq), torch.float32, k_cache)
-    scale = float(scale if scale is not None else D ** -0.5)
-    _here(q, "q")
-    with _on(stream):
-        o = torch.empty((R, Hq, D), dtype=out_dtype, device=q.device) if out is None else out
-        lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-        workspace = _workspace(workspace, decode_workspace_bytes(R, Hq, heads, D), q)
-        _check(lib.cpattn_decode(_p(q), _p(k_cache), _p(v_cache), _p(block_table), _p(lens), _p(pages), _p(o), _p(lse),
-                                 R, Hq, heads, D, page_size, max_pages, num_pages, budget, scale, _p(kv_amax),
-                                 _p(workspace), workspace.numel() * workspace.element_size(),
-                                 BF16 if dtype == torch.bfloat16 else FP32, code,
-                                 BF16 if out_dtype == torch.bfloat16 else FP32, _stream(stream)), "cpattn_decode")
+    s = _here(q, "q", dev)
+    need = _decode_need.get((dev, Hq, heads, D))
+    if need is None:
+        need = _decode_need[dev, Hq, heads, D] = decode_workspace_bytes(R, Hq, heads, D)
+    o = torch.empty_like(q, dtype=out_dtype) if out is None else out
+    lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+    workspace = _workspace(workspace, need, q)
+    _check(lib.cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                             lens.data_ptr(), _p(pages), o.data_ptr(), lse.data_ptr(), R, Hq, heads, D, page_size,
+                             max_pages, num_pages, budget, D ** -0.5 if scale is None else scale, _p(kv_amax),
+                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                             FP32 if dtype == torch.float32 else BF16, code,
+                             FP32 if out_dtype == torch.float32 else BF16, s), "cpattn_decode")
     return o, lse
 
 

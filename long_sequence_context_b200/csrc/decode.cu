@@ -3,11 +3,11 @@
 //     x_j = scale * q_i . k_j,   o_i = sum_j softmax_j(x) v_j,   lse_i = log sum_j e^{x_j}
 // over the request's keys, or over the pages that a list selects.
 //
-// The keys are cut into units of 64.  All units of all (request, kv head)
-// pairs form one line, which is dealt to the thread blocks in equal
-// contiguous shares: a block finds its share from the lengths alone, on the
-// device, so that a batch of very different lengths keeps every block equally
-// busy and the host needs no length.  A pair that lies inside one block is
+// The keys are cut into units of 64 to 256 (16 KB of keys).  All units of all
+// (request, kv head) pairs, with kPairCost more for each pair, form one line,
+// which is dealt to the thread blocks in equal contiguous shares: a block finds
+// its share from the lengths alone, on the device, so that a batch of very
+// different lengths keeps every block equally busy and the host needs no length.  A pair that lies inside one block is
 // finished there; the others leave one partial result (running maximum, sum,
 // unnormalised output, all fp32) per block, and join_kernel combines them by
 // the log-sum-exp rule of cpattn_merge.
@@ -24,8 +24,8 @@ using namespace paged;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = 64;   // keys of one unit: four chunks of 16
-constexpr int kChunk = 16;  // keys a warp takes at a time; never straddles pages
+constexpr int kChunk = 16;   // keys of one tile; never straddles pages
+constexpr int kPairCost = 4;  // what starting and finishing a pair costs, in units of keys
 constexpr int kMaxGroup = 64;
 
 struct DecodeArgs {
@@ -56,10 +56,13 @@ __device__ __forceinline__ int listed_pages(const DecodeArgs& a, int len) {
   const int held = (int)(((long long)len + (1 << a.shift) - 1) >> a.shift);
   return a.pages ? min(held, a.budget) : held;
 }
+template <int UNIT>
 __device__ __forceinline__ int request_units(const DecodeArgs& a, int len) {
-  const long long keys = a.pages ? (long long)listed_pages(a, len) << a.shift : len;
-  return (int)((keys + kUnit - 1) / kUnit);
+  const unsigned keys = a.pages ? (unsigned)listed_pages(a, len) << a.shift : (unsigned)len;
+  return (int)((keys + UNIT - 1) / UNIT);
 }
+// Length of a pair on the line: its units and what a pair costs by itself.
+__device__ __forceinline__ int pair_weight(int units) { return units == 0 ? 0 : units + kPairCost; }
 
 __device__ __forceinline__ void store_o(const DecodeArgs& a, size_t i, float x) {
   if (a.o_bf16)
@@ -80,6 +83,7 @@ struct FmaTile {
   static constexpr int kQueryBytes = D * 4;  // shared memory of one head's query
   static constexpr float kLift = 0.f, kSlack = 8.f;
   static constexpr int kCtas = NT == 1 ? 3 : 2;  // blocks of an SM
+  static constexpr int kSub = 1;
   static constexpr int kVecs = D / 16;  // 16-byte loads of a lane's quarter of a row
 
   float4 k[2][kVecs];
@@ -189,6 +193,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// Loads whose place in the instruction stream is fixed: left to itself the
+// compiler sinks a prefetch to its use and waits for each load in turn.
+__device__ __forceinline__ void load16(const char* p, uint32_t* w) {
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
+}
+__device__ __forceinline__ void load8(const char* p, uint32_t* w) {
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+}
+
 // MmaTile: bf16 and e4m3 caches on the tensor cores, S^T = K Q^T and O^T = V^T P^T
 // with up to 8 heads as the narrow side, so that a group of few heads wastes
 // little.  K and V go from global memory straight into the operand registers:
@@ -206,7 +221,8 @@ struct MmaTile {
   using CT = C;
   static constexpr bool kHalf = sizeof(C) == 1;
   static constexpr int kQueryBytes = D * 2;
-  static constexpr int kCtas = NT == 1 ? 4 : 3;
+  static constexpr int kCtas = NT == 1 ? 3 : 2;
+  static constexpr int kSub = NT == 1 ? 256 / (D * (int)sizeof(C)) : 1;  // 4 KB of keys at a time
   // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
   // ends at 2^-24, which must be far below the largest weight of a long context.
   static constexpr float kLift = kHalf ? 14.f : 0.f, kSlack = kHalf ? 1.f : 8.f;
@@ -274,27 +290,20 @@ struct MmaTile {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int j = 0; j < kRowVecs; ++j) {
-        const char* at = reinterpret_cast<const char*>(p) + (size_t)(g + 8 * r) * D * sizeof(CT) + j * 64 + t * 16;
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(at));
-        k[r][4 * j] = u.x, k[r][4 * j + 1] = u.y, k[r][4 * j + 2] = u.z, k[r][4 * j + 3] = u.w;
-      }
+      for (int j = 0; j < kRowVecs; ++j)
+        load16(reinterpret_cast<const char*>(p) + (g + 8 * r) * D * (int)sizeof(CT) + j * 64 + t * 16, &k[r][4 * j]);
   }
   __device__ __forceinline__ void load_v(const CT* p) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = 2 * t + (i & 1) + 8 * (i >> 1);
-      const char* row = reinterpret_cast<const char*>(p) + (size_t)key * D * sizeof(CT);
+      const char* row = reinterpret_cast<const char*>(p) + key * D * (int)sizeof(CT);
       if constexpr (kVWords == 2) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + g * 8));
-        v[i][0] = u.x, v[i][1] = u.y;
+        load8(row + g * 8, v[i]);
       } else {
 #pragma unroll
-        for (int h = 0; h < kVWords / 4; ++h) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + h * 128 + g * 16));
-          v[i][4 * h] = u.x, v[i][4 * h + 1] = u.y, v[i][4 * h + 2] = u.z, v[i][4 * h + 3] = u.w;
-        }
+        for (int h = 0; h < kVWords / 4; ++h) load16(row + h * 128 + g * 16, &v[i][4 * h]);
       }
     }
   }
@@ -397,21 +406,26 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
   __shared__ long long s_scan[kWarps], s_base;
   __shared__ int s_r;
 
+  constexpr int SUB = Tile::kSub;                // tiles a warp takes at a time
+  constexpr int UNIT = kWarps * SUB * kChunk;    // keys of one unit
+
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its places
 
   // requests without a key: o = 0, lse = -inf
   for (int r = cta; r < a.R; r += gridDim.x) {
-    if (request_units(a, request_len(a, r, tid == 0)) != 0) continue;
+    if (request_units<UNIT>(a, request_len(a, r, tid == 0)) != 0) continue;
     for (int i = tid; i < a.Hq * D; i += kThreads) store_o(a, (size_t)r * a.Hq * D + i, 0.f);
     for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)r * a.Hq + i] = -INFINITY;
   }
 
-  // this block's share of the line of units
+  // this block's share of the line
+  auto weight = [&](int r) { return (long long)pair_weight(request_units<UNIT>(a, request_len(a, r, false))) * a.Hkv; };
   const int per = (a.R + kThreads - 1) / kThreads;
   const int r_lo = min(tid * per, a.R), r_hi = min(r_lo + per, a.R);
   long long mine = 0;
-  for (int r = r_lo; r < r_hi; ++r) mine += (long long)request_units(a, request_len(a, r, false)) * a.Hkv;
+  for (int r = r_lo; r < r_hi; ++r) mine += weight(r);
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
     long long base = upto - mine;
     int r = r_lo;
     for (;; ++r) {
-      const long long n = (long long)request_units(a, request_len(a, r, false)) * a.Hkv;
+      const long long n = weight(r);
       if (u < base + n) break;
       base += n;
     }
@@ -458,14 +472,18 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
 
   while (u < u_end) {
     const int len = request_len(a, r, false);
-    const int n_units = request_units(a, len);
-    if (n_units == 0 || u >= base + (long long)n_units * a.Hkv) {
-      base += (long long)n_units * a.Hkv;
+    const int n_units = request_units<UNIT>(a, len), w_pair = pair_weight(n_units);
+    if (u >= base + (long long)w_pair * a.Hkv) {
+      base += (long long)w_pair * a.Hkv;
       ++r;
       continue;
     }
-    const int h = (int)((u - base) / n_units), x0 = (int)((u - base) % n_units);
-    const int x1 = (int)min((long long)n_units, x0 + (u_end - u));
+    const int h = (int)((u - base) / w_pair), y0 = (int)((u - base) % w_pair);
+    const int y1 = (int)min((long long)w_pair, y0 + (u_end - u));
+    u += y1 - y0;
+    // the pair's own cost stands before its units
+    const int x0 = max(0, y0 - kPairCost), x1 = max(0, y1 - kPairCost);
+    if (x0 == x1) continue;
     const int n_list = listed_pages(a, len);
     const int32_t* table = a.table + (size_t)r * a.max_pages;
     const int32_t* list = a.pages ? a.pages + ((size_t)r * a.Hkv + h) * a.budget : nullptr;
@@ -494,13 +512,14 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
       for (int i = 0; i < 2; ++i)
         unit[nt][i] = scale_log2 * (sizeof(CT) == 1 ? s_unit[hg * HT + nt * 8 + 2 * t + i] : 1.f);
 
-    // Chunk c of the pair: its first row in the cache and how many of its 16 keys
-    // count; chunks that are not there read row 0 and count none.
+    // Tile c of the pair: its first row in the cache and how many of its 16 keys
+    // count; tiles that are not there read row 0 and count none.
+    const int c_end = x1 * kWarps * SUB;
     auto locate = [&](int c, int& n_valid) -> size_t {
       n_valid = 0;
-      const int j = (int)(((long long)c * kChunk) >> a.shift);
-      if (c >= x1 * 4 || j >= n_list) return 0;
-      const int off = (c * kChunk) & ((1 << a.shift) - 1);
+      const int j = (int)((unsigned)c * kChunk >> a.shift);
+      if (c >= c_end || j >= n_list) return 0;
+      const int off = (int)((unsigned)c * kChunk) & ((1 << a.shift) - 1);
       const int logical = list ? list[j] : j;
       const long long pos = ((long long)logical << a.shift) + off;
       if (logical < 0 || pos >= len) return 0;  // padding of the list, or behind the end
@@ -513,32 +532,45 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
       return ((((size_t)page * a.Hkv + h) << a.shift) + off) * D;
     };
 
-    // K of the next chunk is on its way while this one's softmax and output run;
-    // where it stands is known one chunk earlier still.
-    Tile tile;
+    // The next tiles' K is on its way while these ones' softmax and output run;
+    // where they stand is known one step earlier still.
+    Tile tile[SUB];
     const CT* kc = static_cast<const CT*>(a.k);
     const CT* vc = static_cast<const CT*>(a.v);
-    int c = x0 * 4 + kw, n_valid, n_next;
-    size_t row = locate(c, n_valid), row_next = locate(c + kwarps, n_next);
-    if (c < x1 * 4) tile.load_k(kc + row);
-    for (; c < x1 * 4; c += kwarps) {
-      tile.load_v(vc + row);
-      int n_after;
-      const size_t row_after = locate(c + 2 * kwarps, n_after);
-      float s[NT][4];
-      tile.scores(s_q, s);
-      if (c + kwarps < x1 * 4) tile.load_k(kc + row_next);
+    const int step = kwarps * SUB;
+    int c = x0 * kWarps * SUB + kw * SUB, n_valid[SUB], n_next[SUB];
+    size_t row[SUB], row_next[SUB];
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) row[i] = locate(c + i, n_valid[i]);
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) row_next[i] = locate(c + step + i, n_next[i]);
+    if (c < c_end)
+#pragma unroll
+      for (int i = 0; i < SUB; ++i) tile[i].load_k(kc + row[i]);
+    for (; c < c_end; c += step) {
+      float s[SUB][NT][4];
+#pragma unroll
+      for (int i = 0; i < SUB; ++i) tile[i].load_v(vc + row[i]);
+#pragma unroll
+      for (int i = 0; i < SUB; ++i) tile[i].scores(s_q, s[i]);
+      if (c + step < c_end)
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) tile[i].load_k(kc + row_next[i]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = (g + 8 * (i >> 1)) < n_valid ? s[nt][i] * unit[nt][i & 1] : -INFINITY;
-        float mx[2];
+        for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mx[i] = fmaxf(s[nt][i], s[nt][i + 2]);
+          for (int i = 0; i < 4; ++i) {
+            float& x = s[sub][nt][i];
+            x = (g + 8 * (i >> 1)) < n_valid[sub] ? x * unit[nt][i & 1] : -INFINITY;
+            mx[i & 1] = fmaxf(mx[i & 1], x);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-        }
         // the reference of the weights follows the maximum only when that has grown by kSlack
         if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + (Tile::kLift + Tile::kSlack) ||
                                         mx[1] > m[nt][1] + (Tile::kLift + Tile::kSlack))) {
@@ -555,17 +587,26 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float b = m[nt][i & 1];
-          s[nt][i] = exp2f(s[nt][i] - (b == -INFINITY ? 0.f : b));
-          l[nt][i & 1] += s[nt][i];
-        }
+        for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float b = m[nt][i & 1];
+            float& x = s[sub][nt][i];
+            x = exp2f(x - (b == -INFINITY ? 0.f : b));
+            l[nt][i & 1] += x;
+          }
       }
-      tile.output(s, n_valid, acc);
-      row = row_next;
-      n_valid = n_next;
-      row_next = row_after;
-      n_next = n_after;
+#pragma unroll
+      for (int i = 0; i < SUB; ++i) tile[i].output(s[i], n_valid[i], acc);
+      int n_after[SUB];
+      size_t row_after[SUB];
+#pragma unroll
+      for (int i = 0; i < SUB; ++i) row_after[i] = locate(c + 2 * step + i, n_after[i]);
+#pragma unroll
+      for (int i = 0; i < SUB; ++i) {
+        row[i] = row_next[i], n_valid[i] = n_next[i];
+        row_next[i] = row_after[i], n_next[i] = n_after[i];
+      }
     }
 
     // the warps' results side by side, then one per head
@@ -611,18 +652,18 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
     }
     if (!whole && x0 == 0) {
       // the block that holds the pair's last unit: the largest c with total * c / n_cta <= last
-      const long long last = base + (long long)(h + 1) * n_units - 1;
+      const long long last = base + (long long)(h + 1) * w_pair - 1;
       tail = make_int4(r, h, (int)(((last + 1) * n_cta - 1) / total), 0);
     }
-    u += x1 - x0;
   }
   if (tid == 0) a.tail[cta] = tail;
 }
 
 // Combines the partial results of the pair that starts in block blockIdx.x and
 // continues in the following ones: M = max m_c, o = sum e^{m_c - M} o_c / sum
-// e^{m_c - M} l_c.  A warp takes every kJoinWarps / heads-th part of a head.
-constexpr int kJoinWarps = 16;
+// e^{m_c - M} l_c.  Four heads for each blockIdx.y, four warps for each head,
+// every fourth part for each warp.
+constexpr int kJoinHeads = 4, kJoinWays = 4, kJoinWarps = kJoinHeads * kJoinWays;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -632,45 +673,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int first = blockIdx.x, n_parts = tail.z - first + 1;
   constexpr int V = D / 32;
-  int ways = 1;  // warps that share a head
-  while (ways * 2 * a.group <= kJoinWarps) ways *= 2;
-  const int at_once = kJoinWarps / ways;
-  for (int h0 = 0; h0 < a.group; h0 += at_once) {
-    const int head = h0 + warp / ways, way = warp % ways;
-    float m = -INFINITY, l = 0.f, o[V] = {};
-    if (head < a.group) {
-      for (int c = way; c < n_parts; c += ways) {
-        const size_t slot = c == 0 ? 2 * first + 1 : 2 * (first + c);
-        const size_t at = slot * a.group + head;
-        const float mc = a.part_ml[at * 2], lc = a.part_ml[at * 2 + 1];
-        const float mn = fmaxf(m, mc), b = mn == -INFINITY ? 0.f : mn;
-        const float f0 = exp2f(m - b), f1 = exp2f(mc - b);
-        m = mn;
-        l = l * f0 + lc * f1;
+  const int head = blockIdx.y * kJoinHeads + warp / kJoinWays, way = warp % kJoinWays;
+  auto part = [&](int c) { return (size_t)(c == 0 ? 2 * first + 1 : 2 * (first + c)) * a.group + head; };
+  float m = -INFINITY, l = 0.f, o[V] = {};
+  if (head < a.group) {
+    for (int c = way + kJoinWays * lane; c < n_parts; c += kJoinWays * 32) m = fmaxf(m, a.part_ml[part(c) * 2]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = o[e] * f0 + a.part_o[at * D + e * 32 + lane] * f1;
-      }
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float b = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int c = way; c < n_parts; c += kJoinWays) {
+      const size_t at = part(c);
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+      const float f = exp2f(ml.x - b);
+      l = fmaf(f, ml.y, l);
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = fmaf(f, a.part_o[at * D + e * 32 + lane], o[e]);
     }
-    __syncthreads();
+  }
 #pragma unroll
-    for (int e = 0; e < V; ++e) s_o[warp][e * 32 + lane] = o[e];
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-    __syncthreads();
-    if (way == 0 && head < a.group) {
-      float mm = -INFINITY, ll = 0.f, oo[V] = {};
-      for (int w = 0; w < ways; ++w) mm = fmaxf(mm, s_m[warp + w]);
-      const float b = mm == -INFINITY ? 0.f : mm;
-      for (int w = 0; w < ways; ++w) {
-        const float f = exp2f(s_m[warp + w] - b);
-        ll += f * s_l[warp + w];
+  for (int e = 0; e < V; ++e) s_o[warp][e * 32 + lane] = o[e];
+  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+  __syncthreads();
+  if (way == 0 && head < a.group) {
+    float mm = -INFINITY, ll = 0.f, oo[V] = {};
 #pragma unroll
-        for (int e = 0; e < V; ++e) oo[e] += f * s_o[warp + w][e * 32 + lane];
-      }
-      const size_t out = (size_t)tail.x * a.Hq + (size_t)tail.y * a.group + head;
+    for (int w = 0; w < kJoinWays; ++w) mm = fmaxf(mm, s_m[warp + w]);
+    const float b = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-      for (int e = 0; e < V; ++e) store_o(a, out * D + e * 32 + lane, ll == 0.f ? 0.f : oo[e] / ll);
-      if (lane == 0) a.lse[out] = ll == 0.f ? -INFINITY : (b + log2f(ll)) * 0.69314718055994531f;
+    for (int w = 0; w < kJoinWays; ++w) {
+      const float f = exp2f(s_m[warp + w] - b);
+      ll = fmaf(f, s_l[warp + w], ll);
+#pragma unroll
+      for (int e = 0; e < V; ++e) oo[e] = fmaf(f, s_o[warp + w][e * 32 + lane], oo[e]);
     }
+    const size_t out = (size_t)tail.x * a.Hq + (size_t)tail.y * a.group + head;
+#pragma unroll
+    for (int e = 0; e < V; ++e) store_o(a, out * D + e * 32 + lane, ll == 0.f ? 0.f : oo[e] / ll);
+    if (lane == 0) a.lse[out] = ll == 0.f ? -INFINITY : (b + log2f(ll)) * 0.69314718055994531f;
   }
 }
 
@@ -703,7 +743,7 @@ int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
   if (cudaGetLastError() != cudaSuccess) return -1;
   // the join starts while the last blocks finish and waits for them on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(grid, (a.group + kJoinHeads - 1) / kJoinHeads);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
@@ -794,7 +834,7 @@ int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o_bf16 = o_dtype == CPATTN_BF16;
   const long long listed = pages ? std::min(budget, max_pages) : max_pages;
-  const long long max_units = (long long)R * Hkv * (((listed << shift) + kUnit - 1) / kUnit);
+  const long long max_units = (long long)R * Hkv * (((listed << shift) + kWarps * kChunk - 1) / (kWarps * kChunk) + kPairCost);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   const int n = D == 64 ? launch_decode<64>(a, cache_dtype, s, max_units, ws)
