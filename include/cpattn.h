@@ -418,7 +418,7 @@ int cpattn_cache_append(const void* k_new, const void* v_new, long k_tok_stride,
  *                  largest scores, ascending, ties to the lower page, -1 behind the
  *                  last; the newest page and the first keep_first pages are always
  *                  among them.  All pages where a request has no more than budget
- * Preconditions: budget > keep_first >= 0, max_pages <= 262144.
+ * Preconditions: budget > keep_first >= 0, max_pages <= 49152.
  */
 int cpattn_select_pages(const void* q, const void* k_bounds, const int32_t* block_table,
                         const int32_t* lens, int32_t* pages, int R, int Hq, int Hkv, int D,

@@ -10,10 +10,13 @@
 // scores are listed in ascending order, ties to the lower page; the newest
 // page and the first keep_first pages are always among them.
 //
-// One cluster of thread blocks takes one (request, kv head): each block scores
-// a stretch of pages and keeps the scores in its shared memory; the threshold
-// is found by four passes of an 8-bit radix search whose histograms the blocks
-// read from one another.
+// One cluster of thread blocks takes one (request, kv head): every block scores
+// a stretch of pages and sends the scores to the first block's shared memory,
+// which finds the threshold by a radix search of eight bits at a time and lists
+// the pages.  A page's bounds are read once; what bounds the kernel is the
+// chain of latencies from the lengths over the page table and the bounds to the
+// search, so the loads of a warp's next pages are under way while it sums, and
+// the pages are spread over as many blocks as the device holds at once.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -31,9 +34,8 @@ using namespace paged;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeads = 8;       // query heads scored at a time
-constexpr int kPerCta = 32768;  // scores a block can hold
-constexpr int kMaxCluster = 8;
+constexpr int kMaxPages = 49152;  // scores that a block's shared memory holds
+constexpr int kMaxCluster = 16;
 
 struct SelectArgs {
   const void *q, *bounds;
@@ -50,26 +52,29 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// E elements of a row of bounds, as 64-bit numbers
-template <typename CT, int E>
-__device__ __forceinline__ void load_wide(const CT* p, double (&f)[E]) {
-  constexpr int W = E * (int)sizeof(CT) / 4, P = Unpack<CT>::kPerWord;
+// A lane's eighth of a row of bounds, packed.
+template <int W>
+__device__ __forceinline__ void load_packed(const void* p, uint32_t (&w)[W]) {
+  if constexpr (W == 2) {
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    float x[P];
-    Unpack<CT>::word(__ldg(reinterpret_cast<const uint32_t*>(p) + i), x);
-#pragma unroll
-    for (int e = 0; e < P; ++e) f[i * P + e] = (double)x[e];
+    for (int i = 0; i < W; i += 4)
+      asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "l"(static_cast<const char*>(p) + 4 * i));
   }
 }
 
-template <typename CT, int D>
+// NH: query heads scored at a time (a power of two, at least the group or 8)
+template <typename CT, int D, int NH>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   constexpr int E = D / 8;  // columns of one lane; eight lanes share a page
-  extern __shared__ uint32_t s_key[];
-  __shared__ double2 s_q[kHeads][E][8];  // (min(q, 0), max(q, 0)) of column 8 lanes apart
+  constexpr int W = E * (int)sizeof(CT) / 4;
+  extern __shared__ uint32_t s_key[];    // the first block's: the keys of all pages
+  __shared__ double2 s_q[NH][E][8];      // (min(q, 0), max(q, 0)) of column e of each lane
   __shared__ uint32_t s_hist[4][256];
-  __shared__ uint32_t s_count[2], s_pick[2], s_warp[2][kWarps];
+  __shared__ uint32_t s_pick[3], s_warp[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int pair = blockIdx.x / ranks, r = pair / a.Hkv, h = pair % a.Hkv;
@@ -88,13 +93,30 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     return;
   }
 
+  cluster.barrier_arrive();  // no block writes to the first one before that has started
+
   const int per = (held + ranks - 1) / ranks;
   const int first = min(rank * per, held), n = min(per, held - first);
-  for (int i = tid; i < 4 * 256; i += kThreads) (&s_hist[0][0])[i] = 0;
   const int sub = lane & 7;
-  for (int h0 = 0; h0 < a.group; h0 += kHeads) {
+  uint32_t* keys = cluster.map_shared_rank(s_key, 0);
+  const int32_t* table = a.table + (size_t)r * a.max_pages + first;
+  auto page_of = [&](int i) { return table[min(i, n - 1)]; };  // only for n > 0
+  auto load = [&](int page, uint32_t (&lo)[W], uint32_t (&hi)[W]) {
+    const int p = page >= 0 && page < a.num_pages ? page : 0;
+    const CT* b = static_cast<const CT*>(a.bounds) + ((size_t)p * a.Hkv + h) * 2 * D + sub * E;
+    load_packed(b, lo);
+    load_packed(b + D, hi);
+  };
+  for (int h0 = 0; h0 < a.group; h0 += NH) {
+    uint32_t lo[W], hi[W];
+    int i0 = warp * 4, page = 0, page_next = 0;
+    if (i0 < n) {
+      page = page_of(i0 + (lane >> 3));
+      page_next = page_of(i0 + kWarps * 4 + (lane >> 3));
+      load(page, lo, hi);
+    }
     __syncthreads();
-    for (int i = tid; i < kHeads * D; i += kThreads) {
+    for (int i = tid; i < NH * D; i += kThreads) {
       const int head = i / D, d = i % D;
       float x = 0.f;
       if (h0 + head < a.group) {
@@ -104,147 +126,143 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       }
       s_q[head][d % E][d / E] = make_double2(fminf(x, 0.f), fmaxf(x, 0.f));
     }
+    if (h0 == 0) cluster.barrier_wait();
     __syncthreads();
-    for (int i0 = warp * 4; i0 < n; i0 += kWarps * 4) {
-      const int i = i0 + (lane >> 3);
-      const int j = min(first + i, held - 1);
-      const int page = a.table[(size_t)r * a.max_pages + j];
+    for (; i0 < n; i0 += kWarps * 4) {
+      const int i = i0 + (lane >> 3), j = first + i;
       const bool there = page >= 0 && page < a.num_pages;
-      double acc[kHeads] = {};
-      if (there) {
-        const CT* b = static_cast<const CT*>(a.bounds) + ((size_t)page * a.Hkv + h) * 2 * D + sub * E;
-        double lo[E], hi[E];
-        load_wide<CT, E>(b, lo);
-        load_wide<CT, E>(b + D, hi);
+      if (!there && sub == 0) atomicOr(a.err, kErrPage);
+      constexpr int P = Unpack<CT>::kPerWord;
+      float flo[E], fhi[E];
 #pragma unroll
-        for (int m = 0; m < kHeads; ++m)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const double2 q = s_q[m][e][sub];
-            acc[m] = fma(q.x, lo[e], acc[m]);
-            acc[m] = fma(q.y, hi[e], acc[m]);
-          }
-      } else if (sub == 0) {
-        atomicOr(a.err, kErrPage);
+      for (int w = 0; w < W; ++w) {
+        Unpack<CT>::word(lo[w], flo + w * P);
+        Unpack<CT>::word(hi[w], fhi + w * P);
       }
-      // eight lanes, eight heads: lane `sub` is left with head sub
-      double b4[4], b2[2];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const double keep = (sub & 4) ? acc[4 + m] : acc[m], give = (sub & 4) ? acc[m] : acc[4 + m];
-        b4[m] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+      page = page_next;
+      if (i0 + kWarps * 4 < n) {
+        load(page, lo, hi);
+        page_next = page_of(i0 + 2 * kWarps * 4 + (lane >> 3));
       }
+      double acc[NH] = {};
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const double keep = (sub & 2) ? b4[2 + m] : b4[m], give = (sub & 2) ? b4[m] : b4[2 + m];
-        b2[m] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+      for (int e = 0; e < E; ++e) {
+        const double dl = (double)flo[e], dh = (double)fhi[e];
+#pragma unroll
+        for (int m = 0; m < NH; ++m) {
+          const double2 q = s_q[m][e][sub];
+          acc[m] = fma(q.x, dl, acc[m]);
+          acc[m] = fma(q.y, dh, acc[m]);
+        }
       }
-      const double keep = (sub & 1) ? b2[1] : b2[0], give = (sub & 1) ? b2[0] : b2[1];
-      const float x = (float)(keep + __shfl_xor_sync(0xffffffffu, give, 1));
-      uint32_t key = h0 + sub < a.group && there ? order_key(x) : 0u;
+      // the eight lanes' sums: while there are heads to split, a lane keeps half of them
+#pragma unroll
+      for (int o = 4, k = NH; o > 0; o >>= 1) {
+        if (k > 1) {
+          k >>= 1;
+#pragma unroll
+          for (int m = 0; m < NH / 2; ++m)
+            if (m < k) {
+              const double keep = (sub & o) ? acc[k + m] : acc[m], give = (sub & o) ? acc[m] : acc[k + m];
+              acc[m] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        } else {
+          acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+        }
+      }
+      const int head = sub / (8 / NH);  // the head whose sum the lane is left with
+      uint32_t key = h0 + head < a.group && there ? order_key((float)acc[0]) : 0u;
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
       if (sub == 0 && i < n) {
         if (j < a.keep_first || j == held - 1) key = 0xffffffffu;
-        s_key[i] = h0 == 0 ? key : max(key, s_key[i]);
+        keys[j] = h0 == 0 ? key : max(key, keys[j]);
       }
     }
   }
-  __syncthreads();
+  cluster.sync();
+  if (rank != 0) return;
 
   // the budget-th largest key, eight bits at a time
-  uint32_t prefix = 0;
-  int need = a.budget;  // keys wanted among those that share the prefix
+  for (int i = tid; i < 4 * 256; i += kThreads) (&s_hist[0][0])[i] = 0;
+  __syncthreads();
+  uint32_t prefix = 0;     // of the threshold
+  int need = a.budget;     // keys wanted among those that share the prefix
+  uint32_t threshold = 0;  // every key above it, and `need` equal to it
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int low = 24 - 8 * pass;
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < held; i += kThreads) {
       const uint32_t key = s_key[i];
       if (pass == 0 || (key >> (low + 8)) == prefix) atomicAdd(&s_hist[pass][(key >> low) & 255u], 1u);
     }
-    cluster.sync();
-    // thread b: keys in bin 255 - b over the cluster; inclusive sums from the top
-    uint32_t c = 0;
-    for (int k = 0; k < ranks; ++k) c += *cluster.map_shared_rank(&s_hist[pass][255 - tid], k);
+    __syncthreads();
+    // thread b: keys in bin 255 - b; inclusive sums from the top
+    const uint32_t c = s_hist[pass][255 - tid];
     uint32_t up = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += x;
     }
-    if (lane == 31) s_warp[0][warp] = up;
+    if (lane == 31) s_warp[warp] = up;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) up += s_warp[0][w];
-    if (up >= (uint32_t)need && up - c < (uint32_t)need) s_pick[0] = 255 - tid, s_pick[1] = need - (up - c);
+    for (int w = 0; w < warp; ++w) up += s_warp[w];
+    if (up >= (uint32_t)need && up - c < (uint32_t)need) s_pick[0] = 255 - tid, s_pick[1] = need - (up - c), s_pick[2] = c;
     __syncthreads();
     prefix = (prefix << 8) | s_pick[0];
     need = (int)s_pick[1];
-    __syncthreads();
+    threshold = prefix << low;
+    if (low > 0 && s_pick[2] == (uint32_t)need) {  // the whole bin is taken (held > budget: threshold > 0)
+      threshold -= 1;
+      need = 0;
+      break;
+    }
   }
 
-  // every key above the threshold, and the first `need` equal to it
-  if (tid < 2) s_count[tid] = 0;
-  __syncthreads();
-  uint32_t above = 0, equal = 0;
-  for (int i = tid; i < n; i += kThreads) above += s_key[i] > prefix, equal += s_key[i] == prefix;
+  // every key above the threshold and the first `need` equal to it, a stretch of pages for each thread
+  const int stretch = (held + kThreads - 1) / kThreads;
+  const int i0 = min(tid * stretch, held), i1 = min(i0 + stretch, held);
+  uint32_t mine = 0;  // keys above (high half) and equal (low half): at most kMaxPages of each
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t key = s_key[i];
+    mine += key > threshold ? 0x10000u : (key == threshold ? 1u : 0u);
+  }
+  uint32_t up = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    above += __shfl_xor_sync(0xffffffffu, above, o);
-    equal += __shfl_xor_sync(0xffffffffu, equal, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += x;
   }
-  if (lane == 0) {
-    atomicAdd(&s_count[0], above);
-    atomicAdd(&s_count[1], equal);
+  __syncthreads();  // s_warp of the last pass is read
+  if (lane == 31) s_warp[warp] = up;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) up += s_warp[w];
+  up -= mine;
+  uint32_t above = up >> 16, equal = up & 0xffffu;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t key = s_key[i];
+    if (key > threshold || (key == threshold && equal < (uint32_t)need))
+      out[above + min(equal, (uint32_t)need)] = i;
+    above += key > threshold;
+    equal += key == threshold;
   }
-  cluster.sync();
-  uint32_t above_before = 0, equal_before = 0;
-  for (int k = 0; k < rank; ++k) {
-    above_before += *cluster.map_shared_rank(&s_count[0], k);
-    equal_before += *cluster.map_shared_rank(&s_count[1], k);
-  }
-  uint32_t at = above_before + min(equal_before, (uint32_t)need);
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint32_t key = i < n ? s_key[i] : 0u;
-    const bool eq = i < n && key == prefix, gt = i < n && key > prefix;
-    const uint32_t eq_mask = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_warp[0][warp] = __popc(eq_mask);
-    __syncthreads();
-    uint32_t eq_at = equal_before + __popc(eq_mask & ((1u << lane) - 1u));
-    uint32_t eq_all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) eq_at += s_warp[0][w];
-      eq_all += s_warp[0][w];
-    }
-    const bool take = gt || (eq && eq_at < (uint32_t)need);
-    const uint32_t mask = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) s_warp[1][warp] = __popc(mask);
-    __syncthreads();
-    uint32_t to = at + __popc(mask & ((1u << lane) - 1u));
-    uint32_t all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) to += s_warp[1][w];
-      all += s_warp[1][w];
-    }
-    if (take) out[to] = first + i;
-    at += all;
-    equal_before += eq_all;
-    __syncthreads();
-  }
-  cluster.sync();  // no block leaves while another still reads its counts
 }
 
-template <typename CT>
-int launch_select(const SelectArgs& a, int D, int cluster, cudaStream_t s) {
-  static std::atomic<unsigned long long> done64{0}, done128{0};
-  const int bytes = (int)(((a.max_pages + cluster - 1) / cluster) * sizeof(uint32_t));
-  if (D == 64 ? !smem_attr_once(select_kernel<CT, 64>, kPerCta * 4, done64)
-              : !smem_attr_once(select_kernel<CT, 128>, kPerCta * 4, done128))
+template <typename CT, int D, int NH>
+int launch_heads(const SelectArgs& a, int cluster, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  auto* kernel = select_kernel<CT, D, NH>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  if (!(done.load() & (1ull << dev)) &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return -1;
+  if (!smem_attr_once(kernel, kMaxPages * (int)sizeof(uint32_t), done)) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.R * a.Hkv * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
+  cfg.dynamicSmemBytes = a.max_pages * sizeof(uint32_t);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -253,10 +271,21 @@ int launch_select(const SelectArgs& a, int D, int cluster, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   prof_begin(kKSelect, s);
-  const cudaError_t e = D == 64 ? cudaLaunchKernelEx(&cfg, select_kernel<CT, 64>, a)
-                                : cudaLaunchKernelEx(&cfg, select_kernel<CT, 128>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   prof_end(kKSelect, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
+}
+
+template <typename CT, int D>
+int launch_dim(const SelectArgs& a, int cluster, cudaStream_t s) {
+  if (a.group == 1) return launch_heads<CT, D, 1>(a, cluster, s);
+  if (a.group == 2) return launch_heads<CT, D, 2>(a, cluster, s);
+  if (a.group <= 4) return launch_heads<CT, D, 4>(a, cluster, s);
+  return launch_heads<CT, D, 8>(a, cluster, s);
+}
+template <typename CT>
+int launch_select(const SelectArgs& a, int D, int cluster, cudaStream_t s) {
+  return D == 64 ? launch_dim<CT, 64>(a, cluster, s) : launch_dim<CT, 128>(a, cluster, s);
 }
 
 }  // namespace
@@ -273,7 +302,7 @@ extern "C" int cpattn_select_pages(const void* q, const void* k_bounds, const in
   if (cache_dtype != dtype && !(cache_dtype == CPATTN_E4M3 && dtype == CPATTN_BF16)) return CPATTN_ERR_DTYPE;
   const int shift = paged::page_shift(page_size);
   if (R < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 64 || (D != 64 && D != 128)) return CPATTN_ERR_SHAPE;
-  if (shift < 0 || max_pages < 1 || max_pages > kPerCta * kMaxCluster || num_pages < 1) return CPATTN_ERR_SHAPE;
+  if (shift < 0 || max_pages < 1 || max_pages > kMaxPages || num_pages < 1) return CPATTN_ERR_SHAPE;
   if (((long long)max_pages << shift) > 0x7fffffffLL || (long long)R * Hkv > (1LL << 27)) return CPATTN_ERR_SHAPE;
   if (keep_first < 0 || budget < 1 || budget - 1 < keep_first) return CPATTN_ERR_SHAPE;
   if (!q || !k_bounds || !block_table || !lens || !pages) return CPATTN_ERR_ARG;
@@ -301,11 +330,12 @@ extern "C" int cpattn_select_pages(const void* q, const void* k_bounds, const in
   a.q_bf16 = dtype == CPATTN_BF16;
   int dev = 0;
   cudaGetDevice(&dev);
-  // blocks per pair: until the device is full twice over, and while a block
-  // still has at least 64 pages; more where the scores would not fit
+  // blocks per pair: while all blocks fit the device at once (four to an SM), and
+  // a block still has two steps of its warps (64 pages); at most 8 where the
+  // scores leave room for one block to an SM
+  const int most = max_pages > kMaxPages / 2 ? 8 : kMaxCluster;
   int cluster = 1;
-  while (cluster < kMaxCluster && (((long long)a.R * a.Hkv * cluster < 2LL * num_sms(dev) && max_pages > 64 * cluster) ||
-                                   max_pages > kPerCta * cluster))
+  while (cluster < most && (long long)a.R * a.Hkv * cluster * 2 <= 4LL * num_sms(dev) && max_pages > 64 * cluster)
     cluster *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int n = -1;

@@ -124,7 +124,7 @@ def test_select_status_codes():
     def call(R=2, Hq=4, Hkv=2, D=128, P=64, width=8, pages=16, budget=4, keep=1, dtype=0, cache=0, ptr=VP):
         return cp.lib.cpattn_select_pages(ptr, VP, VP, VP, VP, R, Hq, Hkv, D, P, width, pages, budget, keep, dtype, cache, None)
 
-    for kw in (dict(R=0), dict(Hq=5), dict(Hq=130), dict(D=32), dict(P=24), dict(width=0), dict(width=262145), dict(budget=0),
+    for kw in (dict(R=0), dict(Hq=5), dict(Hq=130), dict(D=32), dict(P=24), dict(width=0), dict(width=49153), dict(budget=0),
                dict(budget=1), dict(keep=-1), dict(pages=0), dict(budget=2147483647, keep=2147483647)):
         assert call(**kw) == cp.ERR_SHAPE, kw
     assert call(dtype=3) == cp.ERR_DTYPE and call(dtype=1, cache=2) == cp.ERR_DTYPE
