@@ -52,27 +52,31 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// A lane's eighth of a row of bounds, packed.
+// W consecutive words, in place.
 template <int W>
 __device__ __forceinline__ void load_packed(const void* p, uint32_t (&w)[W]) {
-  if constexpr (W == 2) {
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  } else {
 #pragma unroll
-    for (int i = 0; i < W; i += 4)
-      asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "l"(static_cast<const char*>(p) + 4 * i));
-  }
+  for (int i = 0; i < W; i += 4)
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                 : "l"(static_cast<const char*>(p) + 4 * i));
 }
 
-// NH: query heads scored at a time (a power of two, at least the group or 8)
-template <typename CT, int D, int NH>
+// c (8 pages x 8 heads, 64 bits) += a (8 pages x 4 columns) b (4 columns x 8 heads)
+__device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
+               : "+d"(c[0]), "+d"(c[1])
+               : "d"(a), "d"(b));
+}
+
+template <typename CT, int D>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
-  constexpr int E = D / 8;  // columns of one lane; eight lanes share a page
-  constexpr int W = E * (int)sizeof(CT) / 4;
-  extern __shared__ uint32_t s_key[];    // the first block's: the keys of all pages
-  __shared__ double2 s_q[NH][E][8];      // (min(q, 0), max(q, 0)) of column e of each lane
+  // A warp takes 8 pages at a time, 4 lanes each, in steps of W words (E columns) of
+  // a lane's low and high bounds.
+  constexpr int P = Unpack<CT>::kPerWord;
+  constexpr int W = D / (4 * P) < 8 ? D / (4 * P) : 8, E = W * P, STEPS = D / (4 * E);
+  extern __shared__ uint32_t s_key[];      // the first block's: the keys of all pages
+  __shared__ double2 s_q[STEPS * E][32];   // (min(q, 0), max(q, 0)) of 4 columns x 8 heads
   __shared__ uint32_t s_hist[4][256];
   __shared__ uint32_t s_pick[3], s_warp[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
@@ -97,26 +101,26 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
 
   const int per = (held + ranks - 1) / ranks;
   const int first = min(rank * per, held), n = min(per, held - first);
-  const int sub = lane & 7;
+  const int g = lane >> 2, t = lane & 3;
   uint32_t* keys = cluster.map_shared_rank(s_key, 0);
   const int32_t* table = a.table + (size_t)r * a.max_pages + first;
   auto page_of = [&](int i) { return table[min(i, n - 1)]; };  // only for n > 0
-  auto load = [&](int page, uint32_t (&lo)[W], uint32_t (&hi)[W]) {
+  auto load = [&](int page, int step, uint32_t (&lo)[W], uint32_t (&hi)[W]) {
     const int p = page >= 0 && page < a.num_pages ? page : 0;
-    const CT* b = static_cast<const CT*>(a.bounds) + ((size_t)p * a.Hkv + h) * 2 * D + sub * E;
+    const CT* b = static_cast<const CT*>(a.bounds) + ((size_t)p * a.Hkv + h) * 2 * D + step * 4 * E + t * E;
     load_packed(b, lo);
     load_packed(b + D, hi);
   };
-  for (int h0 = 0; h0 < a.group; h0 += NH) {
+  for (int h0 = 0; h0 < a.group; h0 += 8) {
     uint32_t lo[W], hi[W];
-    int i0 = warp * 4, page = 0, page_next = 0;
+    int i0 = warp * 8, page = 0, page_next = 0;
     if (i0 < n) {
-      page = page_of(i0 + (lane >> 3));
-      page_next = page_of(i0 + kWarps * 4 + (lane >> 3));
-      load(page, lo, hi);
+      page = page_of(i0 + g);
+      page_next = page_of(i0 + kWarps * 8 + g);
+      load(page, 0, lo, hi);
     }
     __syncthreads();
-    for (int i = tid; i < NH * D; i += kThreads) {
+    for (int i = tid; i < 8 * D; i += kThreads) {
       const int head = i / D, d = i % D;
       float x = 0.f;
       if (h0 + head < a.group) {
@@ -124,57 +128,49 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
         x = a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at])
                      : static_cast<const float*>(a.q)[at];
       }
-      s_q[head][d % E][d / E] = make_double2(fminf(x, 0.f), fmaxf(x, 0.f));
+      s_q[d / (4 * E) * E + d % E][head * 4 + d / E % 4] = make_double2(fminf(x, 0.f), fmaxf(x, 0.f));
     }
     if (h0 == 0) cluster.barrier_wait();
     __syncthreads();
-    for (; i0 < n; i0 += kWarps * 4) {
-      const int i = i0 + (lane >> 3), j = first + i;
+    for (; i0 < n; i0 += kWarps * 8) {
+      const int i = i0 + g, j = first + i;
       const bool there = page >= 0 && page < a.num_pages;
-      if (!there && sub == 0) atomicOr(a.err, kErrPage);
-      constexpr int P = Unpack<CT>::kPerWord;
-      float flo[E], fhi[E];
+      if (!there && t == 0) atomicOr(a.err, kErrPage);
+      double acc[4][2] = {};
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        Unpack<CT>::word(lo[w], flo + w * P);
-        Unpack<CT>::word(hi[w], fhi + w * P);
-      }
-      page = page_next;
-      if (i0 + kWarps * 4 < n) {
-        load(page, lo, hi);
-        page_next = page_of(i0 + 2 * kWarps * 4 + (lane >> 3));
-      }
-      double acc[NH] = {};
+      for (int step = 0; step < STEPS; ++step) {
+        float flo[E], fhi[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const double dl = (double)flo[e], dh = (double)fhi[e];
-#pragma unroll
-        for (int m = 0; m < NH; ++m) {
-          const double2 q = s_q[m][e][sub];
-          acc[m] = fma(q.x, dl, acc[m]);
-          acc[m] = fma(q.y, dh, acc[m]);
+        for (int w = 0; w < W; ++w) {
+          Unpack<CT>::word(lo[w], flo + w * P);
+          Unpack<CT>::word(hi[w], fhi + w * P);
         }
-      }
-      // the eight lanes' sums: while there are heads to split, a lane keeps half of them
-#pragma unroll
-      for (int o = 4, k = NH; o > 0; o >>= 1) {
-        if (k > 1) {
-          k >>= 1;
-#pragma unroll
-          for (int m = 0; m < NH / 2; ++m)
-            if (m < k) {
-              const double keep = (sub & o) ? acc[k + m] : acc[m], give = (sub & o) ? acc[m] : acc[k + m];
-              acc[m] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            }
+        if (step + 1 < STEPS) {
+          load(page, step + 1, lo, hi);
         } else {
-          acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+          page = page_next;
+          if (i0 + kWarps * 8 < n) {
+            load(page, 0, lo, hi);
+            page_next = page_of(i0 + 2 * kWarps * 8 + g);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const double2 q = s_q[step * E + e][lane];
+          mma_f64(acc[2 * (e & 1)], (double)flo[e], q.x);
+          mma_f64(acc[2 * (e & 1) + 1], (double)fhi[e], q.y);
         }
       }
-      const int head = sub / (8 / NH);  // the head whose sum the lane is left with
-      uint32_t key = h0 + head < a.group && there ? order_key((float)acc[0]) : 0u;
+      // lane 4g + t has page g with heads 2t and 2t + 1
+      uint32_t key = 0u;
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-      if (sub == 0 && i < n) {
+      for (int m = 0; m < 2; ++m) {
+        const float x = (float)((acc[0][m] + acc[1][m]) + (acc[2][m] + acc[3][m]));
+        if (there && h0 + 2 * t + m < a.group) key = max(key, order_key(x));
+      }
+      key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+      key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
+      if (t == 0 && i < n) {
         if (j < a.keep_first || j == held - 1) key = 0xffffffffu;
         keys[j] = h0 == 0 ? key : max(key, keys[j]);
       }
@@ -249,10 +245,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   }
 }
 
-template <typename CT, int D, int NH>
-int launch_heads(const SelectArgs& a, int cluster, cudaStream_t s) {
+template <typename CT, int D>
+int launch_dim(const SelectArgs& a, int cluster, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  auto* kernel = select_kernel<CT, D, NH>;
+  auto* kernel = select_kernel<CT, D>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
   if (!(done.load() & (1ull << dev)) &&
@@ -276,13 +272,6 @@ int launch_heads(const SelectArgs& a, int cluster, cudaStream_t s) {
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
-template <typename CT, int D>
-int launch_dim(const SelectArgs& a, int cluster, cudaStream_t s) {
-  if (a.group == 1) return launch_heads<CT, D, 1>(a, cluster, s);
-  if (a.group == 2) return launch_heads<CT, D, 2>(a, cluster, s);
-  if (a.group <= 4) return launch_heads<CT, D, 4>(a, cluster, s);
-  return launch_heads<CT, D, 8>(a, cluster, s);
-}
 template <typename CT>
 int launch_select(const SelectArgs& a, int D, int cluster, cudaStream_t s) {
   return D == 64 ? launch_dim<CT, 64>(a, cluster, s) : launch_dim<CT, 128>(a, cluster, s);
