@@ -380,10 +380,11 @@ enum {
  *   verdict        int32[1]: 0, or CPATTN_PLAN_* bits; then nothing changes:
  *                  lens_out = lens, free_state_out = free_state, cu_new 0, slots -1
  * Pages returned by a call can be taken from the next call on.
- * Workspace: cpattn_cache_plan_workspace_bytes(R), 16-byte aligned; contents on
- * entry are ignored; calls that can overlap on the GPU need one each.
+ * Workspace: cpattn_cache_plan_workspace_bytes(R, capacity), 16-byte aligned;
+ * contents on entry are ignored; calls that can overlap on the GPU need one each.
+ * 0 (and NULL) for steps of up to 1024 requests and 4096 tokens.
  */
-size_t cpattn_cache_plan_workspace_bytes(int R);
+size_t cpattn_cache_plan_workspace_bytes(int R, long capacity);
 int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_table, int R,
                       int max_pages, int page_size, int32_t* free_ring, const int32_t* free_state,
                       int num_pages, int32_t* lens_out, int32_t* free_state_out, int32_t* cu_new,

@@ -74,7 +74,7 @@ def _load():
         "cpattn_quantize_e4m3": ([vp, i, i, i, i, i, vp, vp, vp], i),
         "cpattn_fwd_fp8": ([vp] * 6 + [i] * 6 + [f, vp], i),
         "cpattn_layer_bwd": ([vp] * 14 + [i] * 6 + [f, vp, sz, vp], i),
-        "cpattn_cache_plan_workspace_bytes": ([i], sz),
+        "cpattn_cache_plan_workspace_bytes": ([i, l], sz),
         "cpattn_cache_plan": ([vp] * 3 + [i] * 3 + [vp] * 2 + [i] + [vp] * 4 + [l, vp, vp, sz, vp], i),
         "cpattn_cache_append": ([vp] * 2 + [l] * 4 + [vp, l] + [vp] * 3 + [i] * 4 + [vp, i, i, vp], i),
         "cpattn_select_pages": ([vp] * 5 + [i] * 11 + [vp], i),
@@ -551,8 +551,8 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def cache_plan_workspace_bytes(R) -> int:
-    return int(lib.cpattn_cache_plan_workspace_bytes(R))
+def cache_plan_workspace_bytes(R, capacity) -> int:
+    return int(lib.cpattn_cache_plan_workspace_bytes(R, capacity))
 
 
 def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, capacity: int,
@@ -584,16 +584,17 @@ def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, 
     if free_state_out is not None:
         _expect(free_state_out, "free_state_out", (2,), torch.int32, block_table)
     s = _here(block_table, "block_table", dev)
-    need = 4 * (2 * R + 8)  # cpattn_cache_plan_workspace_bytes(R), rounded up
+    need = cache_plan_workspace_bytes(R, capacity)
     lens_out = torch.empty_like(lens) if lens_out is None else lens_out
     free_state_out = torch.empty_like(free_state) if free_state_out is None else free_state_out
     cu_new, verdict = lens.new_empty(R + 1), lens.new_empty(1)
     slots = torch.empty(max(0, capacity), dtype=torch.int64, device=block_table.device)
-    workspace = lens.new_empty(need // 4) if workspace is None else _workspace(workspace, need, block_table)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, block_table)
     _check(lib.cpattn_cache_plan(lens.data_ptr(), delta.data_ptr(), block_table.data_ptr(), R, max_pages, page_size,
                                  free_ring.data_ptr(), free_state.data_ptr(), num_pages, lens_out.data_ptr(),
                                  free_state_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), capacity,
-                                 verdict.data_ptr(), workspace.data_ptr(), need, s), "cpattn_cache_plan")
+                                 verdict.data_ptr(), _p(workspace), need, s), "cpattn_cache_plan")
     return lens_out, free_state_out, cu_new, slots, verdict
 
 

@@ -20,6 +20,11 @@ namespace {
 using namespace paged;
 
 constexpr int kPlanThreads = 1024;
+// One block does the whole plan up to here: a step of one token per request has
+// nothing for a second block, and a second launch costs more than the work.
+// (16 requests: 4 us in one launch, 7 in two.)
+constexpr int kSmallR = 1024;
+constexpr long kSmallTokens = 4096;
 
 // verdict bits of a plan
 constexpr int kShort = 1, kBadLength = 2, kCapacity = 4, kBadState = 8;
@@ -29,8 +34,7 @@ struct PlanArgs {
   int32_t *table, *ring;
   int32_t *lens_out, *state_out, *cu, *verdict;
   int64_t* slots;
-  // workspace: what the planning block leaves for the writing ones
-  int32_t *head, *pop_at, *push_at;  // {ok, ring head, count}, [R + 1], [R + 1]
+  int32_t *head, *pop_at, *push_at;  // workspace of a large plan: see Prefix
   unsigned* err;
   long long capacity;
   int R, max_pages, shift, num_pages;
@@ -38,6 +42,13 @@ struct PlanArgs {
 
 struct Three {
   long long a, b, c;
+};
+
+// What the requests' prefix sums leave for the items, in shared memory (small
+// plans) or in the workspace.
+struct Prefix {
+  int32_t *head;                     // {everything fits, the ring's head, its count}
+  int32_t *cu, *pop_at, *push_at;    // [R + 1]: first new token, page taken, page returned
 };
 
 __device__ __forceinline__ long long pages_of(long long n, int shift) { return (n + (1 << shift) - 1) >> shift; }
@@ -56,7 +67,7 @@ __device__ __forceinline__ Three request_of(const PlanArgs& a, int r, int* bad) 
 // One block: prefix sums over the requests, the verdict, and everything that
 // has one value per request.  Reads all lengths before it writes any, so that
 // lens_out may be lens and state_out free_state.
-__device__ __forceinline__ void plan_requests(const PlanArgs& a) {
+__device__ __forceinline__ void plan_requests(const PlanArgs& a, const Prefix& p) {
   __shared__ Three s_sum[32];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -97,19 +108,19 @@ __device__ __forceinline__ void plan_requests(const PlanArgs& a) {
     const int n = a.lens[r];
     int ignore = 0;
     const Three x = request_of(a, r, &ignore);
-    a.cu[r] = ok ? (int)at.a : 0;
-    a.pop_at[r] = ok ? (int)at.b : 0;
-    a.push_at[r] = ok ? (int)at.c : 0;
+    a.cu[r] = p.cu[r] = ok ? (int)at.a : 0;
+    p.pop_at[r] = ok ? (int)at.b : 0;
+    p.push_at[r] = ok ? (int)at.c : 0;
     a.lens_out[r] = ok ? n + a.delta[r] : n;
     at.a += x.a, at.b += x.b, at.c += x.c;
   }
   if (tid == 0) {
-    a.cu[a.R] = ok ? (int)all.a : 0;
-    a.pop_at[a.R] = ok ? (int)all.b : 0;
-    a.push_at[a.R] = ok ? (int)all.c : 0;
-    a.head[0] = ok;
-    a.head[1] = head;
-    a.head[2] = count;
+    a.cu[a.R] = p.cu[a.R] = ok ? (int)all.a : 0;
+    p.pop_at[a.R] = ok ? (int)all.b : 0;
+    p.push_at[a.R] = ok ? (int)all.c : 0;
+    p.head[0] = ok;
+    p.head[1] = head;
+    p.head[2] = count;
     a.state_out[0] = ok ? (int)(((long long)head + all.b) % a.num_pages) : head;
     a.state_out[1] = ok ? (int)(count - all.b + all.c) : count;
     *a.verdict = verdict;
@@ -128,19 +139,19 @@ __device__ __forceinline__ int find(const int32_t* at, int R, int i) {
 }
 
 // Everything that has one value per token or page, dealt to `n` threads.
-__device__ __forceinline__ void plan_items(const PlanArgs& a, long long i0, long long n) {
-  const bool ok = a.head[0] != 0;
-  const int head = a.head[1], count = a.head[2];
-  const int tokens = a.cu[a.R], pops = a.pop_at[a.R], pushes = a.push_at[a.R];
+__device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, long long i0, long long n) {
+  const bool ok = p.head[0] != 0;
+  const int head = p.head[1], count = p.head[2];
+  const int tokens = p.cu[a.R], pops = p.pop_at[a.R], pushes = p.push_at[a.R];
   for (long long i = i0; i < a.capacity; i += n) {
     long long slot = -1;
     if (i < tokens) {
-      const int r = find(a.cu, a.R, (int)i);
+      const int r = find(p.cu, a.R, (int)i);
       const int before = a.lens_out[r] - a.delta[r];
-      const int pos = before + ((int)i - a.cu[r]);
+      const int pos = before + ((int)i - p.cu[r]);
       const int j = pos >> a.shift, held = (int)pages_of(before, a.shift);
       const int page = j < held ? a.table[(size_t)r * a.max_pages + j]
-                                : a.ring[((long long)head + a.pop_at[r] + (j - held)) % a.num_pages];
+                                : a.ring[((long long)head + p.pop_at[r] + (j - held)) % a.num_pages];
       if (page >= 0 && page < a.num_pages)
         slot = ((long long)page << a.shift) + (pos & ((1 << a.shift) - 1));
       else
@@ -150,23 +161,35 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, long long i0, long
   }
   if (!ok) return;
   for (long long i = i0; i < pops; i += n) {
-    const int r = find(a.pop_at, a.R, (int)i);
+    const int r = find(p.pop_at, a.R, (int)i);
     const int held = (int)pages_of(a.lens_out[r] - a.delta[r], a.shift);
-    a.table[(size_t)r * a.max_pages + held + ((int)i - a.pop_at[r])] = a.ring[((long long)head + i) % a.num_pages];
+    a.table[(size_t)r * a.max_pages + held + ((int)i - p.pop_at[r])] = a.ring[((long long)head + i) % a.num_pages];
   }
   // returned pages go behind the last free one: count + pushes <= num_pages, so
   // none of these places is read above
   for (long long i = i0; i < pushes; i += n) {
-    const int r = find(a.push_at, a.R, (int)i);
+    const int r = find(p.push_at, a.R, (int)i);
     const int left = (int)pages_of(a.lens_out[r], a.shift);
     a.ring[((long long)head + count + i) % a.num_pages] =
-        a.table[(size_t)r * a.max_pages + left + ((int)i - a.push_at[r])];
+        a.table[(size_t)r * a.max_pages + left + ((int)i - p.push_at[r])];
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanArgs a) { plan_requests(a); }
+__global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const PlanArgs a) {
+  __shared__ int32_t s_at[3][kSmallR + 1], s_head[3];
+  const Prefix p = {s_head, s_at[0], s_at[1], s_at[2]};
+  plan_requests(a, p);
+  __syncthreads();
+  plan_items(a, p, threadIdx.x, blockDim.x);
+}
+__global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  plan_requests(a, {a.head, a.cu, a.pop_at, a.push_at});
+}
 __global__ void __launch_bounds__(256) plan_items_kernel(const PlanArgs a) {
-  plan_items(a, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  plan_items(a, {a.head, a.cu, a.pop_at, a.push_at}, (long long)blockIdx.x * blockDim.x + threadIdx.x,
+             (long long)gridDim.x * blockDim.x);
 }
 
 struct AppendArgs {
@@ -180,118 +203,170 @@ struct AppendArgs {
   int Hkv, shift;
 };
 
-template <typename T>
-__device__ __forceinline__ void load_row(const T* p, float (&f)[4]);
-template <>
-__device__ __forceinline__ void load_row<float>(const float* p, float (&f)[4]) {
-  const float4 x = __ldg(reinterpret_cast<const float4*>(p));
-  f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
-}
-template <>
-__device__ __forceinline__ void load_row<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[4]) {
-  const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-  Unpack<__nv_bfloat16>::word(x.x, f);
-  Unpack<__nv_bfloat16>::word(x.y, f + 2);
+// Words of V elements of type T in place; V * sizeof(T) is 8 or 16 bytes.
+template <int B>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[B / 4]) {
+  if constexpr (B == 16)
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+  else
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
 
-// four values as stored, and f as the numbers that are then stored (unscaled)
-template <typename CT>
-struct Store4;
-template <>
-struct Store4<float> {
-  __device__ static __forceinline__ void put(float* p, float (&f)[4], float) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-template <>
-struct Store4<__nv_bfloat16> {
-  __device__ static __forceinline__ void put(__nv_bfloat16* p, float (&f)[4], float) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-    uint2 w;
-    w.x = *reinterpret_cast<const uint32_t*>(&a);
-    w.y = *reinterpret_cast<const uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p) = w;
-  }
-};
-template <>
-struct Store4<E4m3> {
-  __device__ static __forceinline__ void put(E4m3* p, float (&f)[4], float s) {
+// V floats as stored; f becomes the numbers that are then stored (unscaled).
+template <typename CT, int V>
+__device__ __forceinline__ void put(CT* p, float (&f)[V], float s) {
+  if constexpr (sizeof(CT) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __fmul_rn(f[i], s);
-    const uint32_t w = (uint32_t)float2_to_e4m3x2(f[0], f[1]) | ((uint32_t)float2_to_e4m3x2(f[2], f[3]) << 16);
-    *reinterpret_cast<uint32_t*>(p) = w;
-    Unpack<E4m3>::word(w, f);
-  }
-};
-template <typename CT>
-__device__ __forceinline__ void load4(const CT* p, float (&f)[4]) {
-  constexpr int W = (int)sizeof(CT);  // words of four elements
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  } else if constexpr (sizeof(CT) == 2) {
+    uint32_t w[V / 2];
 #pragma unroll
-  for (int i = 0; i < W; ++i) Unpack<CT>::word(w[i], f + i * (4 / W));
+    for (int i = 0; i < V / 2; ++i) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      w[i] = (uint32_t)float2_to_e4m3x2(__fmul_rn(f[4 * i], s), __fmul_rn(f[4 * i + 1], s)) |
+             ((uint32_t)float2_to_e4m3x2(__fmul_rn(f[4 * i + 2], s), __fmul_rn(f[4 * i + 3], s)) << 16);
+      Unpack<E4m3>::word(w[i], f + 4 * i);
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
 }
 
-// A group of D / 4 lanes takes the rows of one kv head that lie next to one
-// another in one page, copies them and reduces their keys.
+constexpr int kAppendWarps = 8;
+constexpr int kTile = 32;  // tokens whose slots one block looks at
+
+// The new rows fall into runs: tokens next to one another in one page.  A warp
+// takes a run of one kv head, copies it with kAhead rows' loads under way and
+// reduces its keys.  Blocks (x: 32 tokens; y: a share of their runs and heads)
+// find the runs that begin in their tokens by a vote over the slots.
 template <typename IT, typename CT, int D>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
-  constexpr int kLanes = D / 4;
-  const long long unit = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
-  const int d = (threadIdx.x % kLanes) * 4;
-  const long long t = unit / a.Hkv;
-  const int h = (int)(unit % a.Hkv);
-  if (t >= a.N) return;
-  const long long slot = a.slots[t];
-  if (slot < 0) return;
-  if (slot >= a.n_slots) {
-    if (d == 0 && h == 0) atomicOr(a.err, kErrPage);
-    return;
-  }
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a) {
+  constexpr int V = 16 / (int)sizeof(IT);  // elements of a lane
+  constexpr int kLanes = D / V, kRows = 32 / kLanes;  // lanes of a row, rows of a warp's load
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int page_mask = (1 << a.shift) - 1;
-  const long long page = slot >> a.shift;
-  const int off = (int)(slot & page_mask);
-  if (t > 0 && off > 0 && a.slots[t - 1] == slot - 1) return;  // the run begins before this row
+  const long long t0 = (long long)blockIdx.x * kTile;
+  const long long mine = t0 + lane < a.N ? a.slots[t0 + lane] : -1;
+  long long before = __shfl_up_sync(0xffffffffu, mine, 1);
+  if (lane == 0) before = t0 > 0 ? a.slots[t0 - 1] : -1;
+  const bool bad = mine >= a.n_slots;
+  if (bad && warp == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPage);
+  const bool first = mine >= 0 && !bad && ((mine & page_mask) == 0 || before != mine - 1);
+  const uint32_t runs = __ballot_sync(0xffffffffu, first);
+  const int nth = __popc(runs & ((1u << lane) - 1u));
   const float ks = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax) : 1.f;
   const float vs = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax + 1) : 1.f;
-  float lo[4], hi[4];
+  const int sub = lane / kLanes, d = lane % kLanes * V;
+
+  const int items = __popc(runs) * a.Hkv;
+  for (int item = blockIdx.y * kAppendWarps + warp; item < items; item += gridDim.y * kAppendWarps) {
+    const int run = item / a.Hkv, h = item % a.Hkv;
+    const int from = __ffs(__ballot_sync(0xffffffffu, first && nth == run)) - 1;
+    const long long t = t0 + from, slot = __shfl_sync(0xffffffffu, mine, from);
+    const int off = (int)(slot & page_mask);
+    // the run's length: up to the page's end
+    const int most = (int)min((long long)(page_mask + 1 - off), a.N - t);
+    int len = 1;
+    for (int i = 1; i < most; i += 32) {
+      const bool on = i + lane < most && a.slots[t + i + lane] == slot + i + lane;
+      const uint32_t gap = ~__ballot_sync(0xffffffffu, on);
+      len = i + (gap ? __ffs(gap) - 1 : 32);
+      if (gap) break;
+    }
+    const IT* k = static_cast<const IT*>(a.k) + t * a.k_tok + h * a.k_head + d;
+    const IT* v = static_cast<const IT*>(a.v) + t * a.v_tok + h * a.v_head + d;
+    const size_t at = ((((size_t)(slot >> a.shift) * a.Hkv + h) << a.shift) + off) * D + d;
+    CT* kc = static_cast<CT*>(a.k_cache) + at;
+    CT* vc = static_cast<CT*>(a.v_cache) + at;
+    float lo[V], hi[V];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) lo[e] = INFINITY, hi[e] = -INFINITY;
-  for (int i = 0; off + i <= page_mask && t + i < a.N; ++i) {
-    if (i > 0 && a.slots[t + i] != slot + i) break;
-    float k[4], v[4];
-    load_row(static_cast<const IT*>(a.k) + (t + i) * a.k_tok + h * a.k_head + d, k);
-    load_row(static_cast<const IT*>(a.v) + (t + i) * a.v_tok + h * a.v_head + d, v);
-    const size_t at = ((((size_t)page * a.Hkv + h) << a.shift) + off + i) * D + d;
-    Store4<CT>::put(static_cast<CT*>(a.k_cache) + at, k, ks);
-    Store4<CT>::put(static_cast<CT*>(a.v_cache) + at, v, vs);
+    for (int e = 0; e < V; ++e) lo[e] = INFINITY, hi[e] = -INFINITY;
+    for (int i0 = sub; i0 < len; i0 += kRows * kAhead) {
+      uint32_t kw[kAhead][4], vw[kAhead][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) lo[e] = fminf(lo[e], k[e]), hi[e] = fmaxf(hi[e], k[e]);
+      for (int x = 0; x < kAhead; ++x) {
+        const int i = i0 + x * kRows;
+        if (i < len) {
+          load_words<16>(k + i * a.k_tok, kw[x]);
+          load_words<16>(v + i * a.v_tok, vw[x]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int i = i0 + x * kRows;
+        if (i < len) {
+          float f[V], g[V];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            Unpack<IT>::word(kw[x][w], f + w * Unpack<IT>::kPerWord);
+            Unpack<IT>::word(vw[x][w], g + w * Unpack<IT>::kPerWord);
+          }
+          put<CT, V>(kc + (size_t)i * D, f, ks);
+          put<CT, V>(vc + (size_t)i * D, g, vs);
+#pragma unroll
+          for (int e = 0; e < V; ++e) lo[e] = fminf(lo[e], f[e]), hi[e] = fmaxf(hi[e], f[e]);
+        }
+      }
+    }
+    if (!a.bounds) continue;
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
+        hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+      }
+    if (sub != 0) continue;
+    CT* b = static_cast<CT*>(a.bounds) + ((size_t)(slot >> a.shift) * a.Hkv + h) * 2 * D + d;
+    if (off > 0) {  // the page held rows before: the first row of a page starts its bounds afresh
+      constexpr int W = V * (int)sizeof(CT) / 4;
+      uint32_t w[2][W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        w[0][i] = reinterpret_cast<const uint32_t*>(b)[i];
+        w[1][i] = reinterpret_cast<const uint32_t*>(b + D)[i];
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        constexpr int P = Unpack<CT>::kPerWord;
+        float f[P], g[P];
+        Unpack<CT>::word(w[0][i], f);
+        Unpack<CT>::word(w[1][i], g);
+#pragma unroll
+        for (int e = 0; e < P; ++e) lo[i * P + e] = fminf(lo[i * P + e], f[e]), hi[i * P + e] = fmaxf(hi[i * P + e], g[e]);
+      }
+    }
+    // stored values: writing them again rounds nothing
+    put<CT, V>(b, lo, 1.f);
+    put<CT, V>(b + D, hi, 1.f);
   }
-  if (!a.bounds) return;
-  CT* b = static_cast<CT*>(a.bounds) + ((size_t)page * a.Hkv + h) * 2 * D + d;
-  if (off > 0) {  // the page held rows before: the first row of a page starts its bounds afresh
-    float f[4];
-    load4<CT>(b, f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) lo[e] = fminf(lo[e], f[e]);
-    load4<CT>(b + D, f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) hi[e] = fmaxf(hi[e], f[e]);
-  }
-  // stored values: writing them again rounds nothing
-  Store4<CT>::put(b, lo, 1.f);
-  Store4<CT>::put(b + D, hi, 1.f);
 }
 
 template <typename IT, typename CT>
 int launch_append(const AppendArgs& a, int D, cudaStream_t s) {
-  const long long threads = a.N * a.Hkv * (D / 4);
-  const unsigned blocks = (unsigned)((threads + 255) / 256);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  // a warp for every token and head while that many fit the device, so that runs of
+  // one token do not queue
+  const long long tiles = (a.N + kTile - 1) / kTile;
+  const long long warps = std::min<long long>(a.N * a.Hkv, (long long)num_sms(dev) * 64);
+  const long long share = std::max<long long>(1, std::min<long long>(65535, (warps + tiles * kAppendWarps - 1) / (tiles * kAppendWarps)));
+  const dim3 grid((unsigned)tiles, (unsigned)share);
   prof_begin(kKCacheAppend, s);
   if (D == 64)
-    append_kernel<IT, CT, 64><<<blocks, 256, 0, s>>>(a);
+    append_kernel<IT, CT, 64><<<grid, kAppendWarps * 32, 0, s>>>(a);
   else
-    append_kernel<IT, CT, 128><<<blocks, 256, 0, s>>>(a);
+    append_kernel<IT, CT, 128><<<grid, kAppendWarps * 32, 0, s>>>(a);
   prof_end(kKCacheAppend, s);
   return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
@@ -303,8 +378,8 @@ using namespace cpattn;
 
 extern "C" {
 
-size_t cpattn_cache_plan_workspace_bytes(int R) {
-  if (R < 1) return 0;
+size_t cpattn_cache_plan_workspace_bytes(int R, long capacity) {
+  if (R < 1 || (R <= kSmallR && capacity <= kSmallTokens)) return 0;
   return (4 + 2 * ((size_t)R + 1)) * sizeof(int32_t);
 }
 
@@ -326,7 +401,8 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
                         (const void*)cu_new, (const void*)verdict})
     if (!paged::aligned_to(p, 4)) return CPATTN_ERR_ALIGN;
   if (!paged::aligned_to(slots, 8)) return CPATTN_ERR_ALIGN;
-  if (!workspace || ws_bytes < cpattn_cache_plan_workspace_bytes(R)) return CPATTN_ERR_WORKSPACE;
+  const size_t need = cpattn_cache_plan_workspace_bytes(R, capacity);
+  if (need && (!workspace || ws_bytes < need)) return CPATTN_ERR_WORKSPACE;
   if (!paged::aligned_to(workspace, 16)) return CPATTN_ERR_ALIGN;
   unsigned* err = device_error_word();
   if (!err) return CPATTN_ERR_CUDA;
@@ -341,9 +417,11 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   a.cu = cu_new;
   a.verdict = verdict;
   a.slots = slots;
-  a.head = static_cast<int32_t*>(workspace);
-  a.pop_at = a.head + 4;
-  a.push_at = a.pop_at + R + 1;
+  if (need) {
+    a.head = static_cast<int32_t*>(workspace);
+    a.pop_at = a.head + 4;
+    a.push_at = a.pop_at + R + 1;
+  }
   a.err = err;
   a.capacity = capacity;
   a.R = R;
@@ -351,6 +429,14 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   a.shift = shift;
   a.num_pages = num_pages;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!need) {
+    prof_begin(kKCachePlan, s);
+    plan_small_kernel<<<1, kPlanThreads, 0, s>>>(a);
+    prof_end(kKCachePlan, s);
+    if (cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
+    add_launches(1);
+    return CPATTN_OK;
+  }
   int dev = 0;
   cudaGetDevice(&dev);
   prof_begin(kKCachePlan, s);
@@ -358,11 +444,19 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   prof_end(kKCachePlan, s);
   if (cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
   const long long items = std::max<long long>(capacity, std::min<long long>((long long)R * max_pages, num_pages));
-  const int blocks = (int)std::min<long long>((items + 255) / 256, (long long)num_sms(dev) * 8);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::max<long long>(1, std::min<long long>((items + 255) / 256, (long long)num_sms(dev) * 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};  // the items' blocks take their places while the requests are summed, and wait
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   prof_begin(kKCachePlan, s);
-  plan_items_kernel<<<std::max(blocks, 1), 256, 0, s>>>(a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_items_kernel, a);
   prof_end(kKCachePlan, s);
-  if (cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
+  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
   add_launches(2);
   return CPATTN_OK;
 }

@@ -139,8 +139,10 @@ def test_plan_status_codes():
         assert call(**kw) == cp.ERR_SHAPE, kw
     assert call(ptr=None) == cp.ERR_ARG and call(slots=None) == cp.ERR_ARG
     assert call(ptr=ctypes.c_void_p(2)) == cp.ERR_ALIGN and call(slots=ctypes.c_void_p(4)) == cp.ERR_ALIGN
-    assert call(ws=None) == cp.ERR_WORKSPACE and call(ws_bytes=cp.cache_plan_workspace_bytes(2) - 1) == cp.ERR_WORKSPACE
-    assert call(ws=ctypes.c_void_p(8)) == cp.ERR_ALIGN and cp.cache_plan_workspace_bytes(0) == 0
+    need = cp.cache_plan_workspace_bytes(2, 5000)
+    assert need > 0 and cp.cache_plan_workspace_bytes(0, 5000) == 0 and cp.cache_plan_workspace_bytes(2, 4) == 0
+    assert call(cap=5000, ws=None) == cp.ERR_WORKSPACE and call(cap=5000, ws_bytes=need - 1) == cp.ERR_WORKSPACE
+    assert call(ws=ctypes.c_void_p(8)) == cp.ERR_ALIGN
 
 
 def test_append_status_codes():
