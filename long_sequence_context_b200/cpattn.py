@@ -481,9 +481,10 @@ def layer_bwd(x, w_qkv, w_o, saved, dy, num_heads: int, cp_size: int, causal: bo
 
 # ---- the paged key-value cache ----
 #
-# One token's step is a handful of calls of some microseconds each, so these
-# checks are kept short: one comparison per tensor, and the message only for a
-# tensor that fails it.
+# One token's step is a handful of calls of some microseconds each, and a check
+# by `_expect` takes about one: these calls compare everything in one expression
+# and look for the argument to name only when that fails.  (torch.empty takes
+# its sizes as separate arguments for the same reason.)
 
 def _fits(t, shape, dtype, dev) -> bool:
     return isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.get_device() == dev \
@@ -517,25 +518,30 @@ def _batch(block_table, lens, like=None):
     """Checks a page table [R, max_pages] and the lengths [R]; returns (R, max_pages)."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a [R, max_pages] tensor")
-    shape = block_table.shape
-    dev = (block_table if like is None else like).get_device()
-    if not _fits(block_table, shape, torch.int32, dev):
-        _expect(block_table, "block_table", shape, torch.int32, like)
-    if not _fits(lens, shape[:1], torch.int32, dev):
-        _expect(lens, "lens", shape[:1], torch.int32, block_table)
-    return shape
+    _expect(block_table, "block_table", block_table.shape, torch.int32, like)
+    _expect(lens, "lens", block_table.shape[:1], torch.int32, block_table)
+    return block_table.shape
 
 
-def _query(q, dtype, R, heads, D, like):
-    """Checks q [R, Hq, D] against the cache it reads; returns Hq."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [R, Hq, D] tensor")
-    Hq = q.shape[1]
-    if not _fits(q, (R, Hq, D), dtype, like.get_device()):
-        _expect(q, "q", (R, Hq, D), dtype, like)
-    if Hq % heads != 0:
-        raise ValueError(f"q has {Hq} heads, not a multiple of the cache's {heads}")
-    return Hq
+def _queries(q, block_table, lens, dtype, heads, D, cache, dev):
+    """Checks q [R, Hq, D] and the batch it belongs to against the cache; returns (R, Hq, max_pages)."""
+    try:
+        (R, max_pages), Hq = block_table.shape, q.shape[1]
+        right = (q.shape == (R, Hq, D) and lens.shape == (R,) and q.dtype is dtype
+                 and block_table.dtype is lens.dtype is torch.int32 and q.get_device() == dev
+                 and block_table.get_device() == dev and lens.get_device() == dev and q.is_contiguous()
+                 and block_table.is_contiguous() and lens.is_contiguous() and Hq % heads == 0)
+    except (AttributeError, TypeError, ValueError, IndexError):
+        right = False
+    if not right:
+        R, max_pages = _batch(block_table, lens, cache)
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a [R, Hq, D] tensor")
+        Hq = q.shape[1]
+        _expect(q, "q", (R, Hq, D), dtype, cache)
+        if Hq % heads != 0:
+            raise ValueError(f"q has {Hq} heads, not a multiple of the cache's {heads}")
+    return R, Hq, max_pages
 
 
 def _here(t, name: str, dev: int):
@@ -545,6 +551,13 @@ def _here(t, name: str, dev: int):
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _scratch(workspace, need, like):
+    workspace = _workspace(workspace, need, like)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
 
 
 def _p(t):
@@ -568,29 +581,37 @@ def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, 
         with torch.cuda.stream(stream):
             return cache_plan(lens, delta, block_table, free_ring, free_state, page_size, capacity, lens_out,
                               free_state_out, workspace)
-    R, max_pages = _batch(block_table, lens)
-    dev = block_table.get_device()
-    if not _fits(delta, (R,), torch.int32, dev):
+    try:
+        (R, max_pages), (num_pages,), dev = block_table.shape, free_ring.shape, block_table.get_device()
+        right = (lens.shape == (R,) and delta.shape == (R,) and free_state.shape == (2,)
+                 and block_table.dtype is lens.dtype is delta.dtype is free_ring.dtype is free_state.dtype is torch.int32
+                 and lens.get_device() == dev and delta.get_device() == dev and free_ring.get_device() == dev
+                 and free_state.get_device() == dev and block_table.is_contiguous() and lens.is_contiguous()
+                 and delta.is_contiguous() and free_ring.is_contiguous() and free_state.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        right = False
+    if not right:
+        R, max_pages = _batch(block_table, lens)
         _expect(delta, "delta", (R,), torch.int32, block_table)
-    if not isinstance(free_ring, torch.Tensor) or free_ring.dim() != 1:
-        raise ValueError("free_ring must be a [num_pages] tensor")
-    num_pages = free_ring.shape[0]
-    if not _fits(free_ring, (num_pages,), torch.int32, dev):
-        _expect(free_ring, "free_ring", (num_pages,), torch.int32, block_table)
-    if not _fits(free_state, (2,), torch.int32, dev):
+        if not isinstance(free_ring, torch.Tensor) or free_ring.dim() != 1:
+            raise ValueError("free_ring must be a [num_pages] tensor")
+        _expect(free_ring, "free_ring", free_ring.shape, torch.int32, block_table)
         _expect(free_state, "free_state", (2,), torch.int32, block_table)
+        num_pages, dev = free_ring.shape[0], block_table.get_device()
     if lens_out is not None:
         _expect(lens_out, "lens_out", (R,), torch.int32, block_table)
     if free_state_out is not None:
         _expect(free_state_out, "free_state_out", (2,), torch.int32, block_table)
     s = _here(block_table, "block_table", dev)
-    need = cache_plan_workspace_bytes(R, capacity)
+    need = lib.cpattn_cache_plan_workspace_bytes(R, capacity)
     lens_out = torch.empty_like(lens) if lens_out is None else lens_out
     free_state_out = torch.empty_like(free_state) if free_state_out is None else free_state_out
     cu_new, verdict = lens.new_empty(R + 1), lens.new_empty(1)
-    slots = torch.empty(max(0, capacity), dtype=torch.int64, device=block_table.device)
-    if need or workspace is not None:
-        workspace = _workspace(workspace, need, block_table)
+    slots = torch.empty(max(0, capacity), dtype=torch.int64, device=lens.device)
+    if workspace is not None:
+        workspace = _scratch(workspace, need, block_table)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=lens.device)
     _check(lib.cpattn_cache_plan(lens.data_ptr(), delta.data_ptr(), block_table.data_ptr(), R, max_pages, page_size,
                                  free_ring.data_ptr(), free_state.data_ptr(), num_pages, lens_out.data_ptr(),
                                  free_state_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), capacity,
@@ -618,15 +639,24 @@ def cache_append_(k_new, v_new, slots, k_cache, v_cache, k_bounds=None, kv_amax=
     contiguous columns (views of [kv_heads, N, D] too), slots [N] int64 (negative:
     skipped).  k_bounds [num_pages, kv_heads, 2, D] is kept up to date when given."""
     (num_pages, heads, page_size, D), dtype, code, dev = _cache(k_cache, v_cache, kv_amax)
-    if k_bounds is not None and not _fits(k_bounds, (num_pages, heads, 2, D), k_cache.dtype, dev):
-        _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_cache.dtype, k_cache)
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-        raise ValueError("slots must be a [N] tensor")
-    N = slots.shape[0]
-    if not _fits(slots, (N,), torch.int64, dev):
+    try:
+        (N,), ks, vs = slots.shape, k_new.stride(), v_new.stride()
+        right = (k_new.shape == (N, heads, D) and v_new.shape == (N, heads, D) and k_new.dtype is v_new.dtype is dtype
+                 and ks[2] == 1 == vs[2] and slots.dtype is torch.int64 and slots.is_contiguous()
+                 and k_new.get_device() == dev and v_new.get_device() == dev and slots.get_device() == dev
+                 and (k_bounds is None or (k_bounds.shape == (num_pages, heads, 2, D) and k_bounds.dtype is k_cache.dtype
+                                           and k_bounds.get_device() == dev and k_bounds.is_contiguous())))
+    except (AttributeError, TypeError, ValueError):
+        right = False
+    if not right:
+        if k_bounds is not None:
+            _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_cache.dtype, k_cache)
+        if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+            raise ValueError("slots must be a [N] tensor")
+        N = slots.shape[0]
         _expect(slots, "slots", (N,), torch.int64, k_cache)
-    ks = _rows(k_new, "k_new", (N, heads, D), dtype, k_cache)
-    vs = _rows(v_new, "v_new", (N, heads, D), dtype, k_cache)
+        ks = _rows(k_new, "k_new", (N, heads, D), dtype, k_cache)
+        vs = _rows(v_new, "v_new", (N, heads, D), dtype, k_cache)
     s = _here(k_cache, "k_cache", dev)
     if stream is not None:
         s = stream.cuda_stream
@@ -652,12 +682,11 @@ def select_pages(q, k_bounds, block_table, lens, page_size: int, budget: int, ke
         raise ValueError(f"k_bounds is empty: {tuple(k_bounds.shape)}")
     if not _fits(k_bounds, (num_pages, heads, 2, D), k_bounds.dtype, dev):
         _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_bounds.dtype)
-    R, max_pages = _batch(block_table, lens, k_bounds)
-    Hq = _query(q, dtype, R, heads, D, k_bounds)
+    R, Hq, max_pages = _queries(q, block_table, lens, dtype, heads, D, k_bounds, dev)
     if budget < 1 or keep_first < 0 or budget <= keep_first:
         raise ValueError(f"budget ({budget}) must be above keep_first ({keep_first}), and keep_first not negative")
     s = _here(q, "q", dev)
-    pages = torch.empty((R, heads, budget), dtype=torch.int32, device=q.device)
+    pages = torch.empty(R, heads, budget, dtype=torch.int32, device=q.device)
     _check(lib.cpattn_select_pages(q.data_ptr(), k_bounds.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
                                    pages.data_ptr(), R, Hq, heads, D, page_size, max_pages, num_pages, budget, keep_first,
                                    FP32 if dtype == torch.float32 else BF16, code, s), "cpattn_select_pages")
@@ -680,8 +709,7 @@ def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, sca
         with torch.cuda.stream(stream):
             return decode(q, k_cache, v_cache, block_table, lens, pages, kv_amax, scale, out_dtype, out, lse, workspace)
     (num_pages, heads, page_size, D), dtype, code, dev = _cache(k_cache, v_cache, kv_amax)
-    R, max_pages = _batch(block_table, lens, k_cache)
-    Hq = _query(q, dtype, R, heads, D, k_cache)
+    R, Hq, max_pages = _queries(q, block_table, lens, dtype, heads, D, k_cache, dev)
     budget = 0
     if pages is not None:
         if not isinstance(pages, torch.Tensor) or pages.dim() != 3:
@@ -700,14 +728,20 @@ def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, sca
     need = _decode_need.get((dev, Hq, heads, D))
     if need is None:
         need = _decode_need[dev, Hq, heads, D] = decode_workspace_bytes(R, Hq, heads, D)
-    o = torch.empty_like(q, dtype=out_dtype) if out is None else out
-    lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-    workspace = _workspace(workspace, need, q)
+    if out is not None:
+        o = out
+    else:
+        o = torch.empty_like(q) if out_dtype is dtype else torch.empty_like(q, dtype=out_dtype)
+    lse = torch.empty(R, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
+    if workspace is None:
+        workspace, ws_bytes = torch.empty(need, dtype=torch.uint8, device=q.device), need
+    else:
+        workspace = _scratch(workspace, need, q)
+        ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib.cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                              lens.data_ptr(), _p(pages), o.data_ptr(), lse.data_ptr(), R, Hq, heads, D, page_size,
                              max_pages, num_pages, budget, D ** -0.5 if scale is None else scale, _p(kv_amax),
-                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                             FP32 if dtype == torch.float32 else BF16, code,
+                             workspace.data_ptr(), ws_bytes, FP32 if dtype == torch.float32 else BF16, code,
                              FP32 if out_dtype == torch.float32 else BF16, s), "cpattn_decode")
     return o, lse
 

@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   constexpr int W = D / (4 * P) < 8 ? D / (4 * P) : 8, E = W * P, STEPS = D / (4 * E);
   extern __shared__ uint32_t s_key[];      // the first block's: the keys of all pages
   __shared__ double2 s_q[STEPS * E][32];   // (min(q, 0), max(q, 0)) of 4 columns x 8 heads
-  __shared__ uint32_t s_hist[4][256];
-  __shared__ uint32_t s_pick[3], s_warp[kWarps];
+  __shared__ uint32_t s_hist[256], s_bin[kThreads];
+  __shared__ uint32_t s_pick[3], s_found, s_warp[kWarps], s_warp2[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int pair = blockIdx.x / ranks, r = pair / a.Hkv, h = pair % a.Hkv;
@@ -179,22 +179,39 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   cluster.sync();
   if (rank != 0) return;
 
-  // the budget-th largest key, eight bits at a time
-  for (int i = tid; i < 4 * 256; i += kThreads) (&s_hist[0][0])[i] = 0;
+  // The pages that are always listed need no search: their key is the largest.
+  // The others: first the leading bits that all keys share, then eight bits at a
+  // time until the bin of the threshold is small enough to rank its keys directly.
+  const int always = min(a.keep_first, held - 1) + 1;
+  const uint32_t kAlways = 0xffffffffu;
+  uint32_t any = 0u, all = 0xffffffffu;
+  for (int i = tid; i < held; i += kThreads) {
+    const uint32_t key = s_key[i];
+    if (key != kAlways) any |= key, all &= key;
+  }
+  s_hist[tid] = 0;
+  any = __reduce_or_sync(0xffffffffu, any);
+  all = __reduce_and_sync(0xffffffffu, all);
+  if (lane == 0) s_warp[warp] = any, s_warp2[warp] = all;
+  if (tid == 0) s_found = 0;
   __syncthreads();
-  uint32_t prefix = 0;     // of the threshold
-  int need = a.budget;     // keys wanted among those that share the prefix
-  uint32_t threshold = 0;  // every key above it, and `need` equal to it
-#pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int low = 24 - 8 * pass;
+  for (int w = 0; w < kWarps; ++w) any |= s_warp[w], all &= s_warp2[w];
+  int low = 32 - __clz(any ^ all);               // bits below `low` differ
+  uint32_t prefix = low < 32 ? any >> low : 0u;  // of the threshold
+  int need = a.budget - always;                  // keys wanted among those that share the prefix
+  uint32_t threshold = any;                      // every key above it, and `need` equal to it
+  if (need == 0) low = 0, threshold = kAlways - 1u;
+  while (low > 0) {
+    const int above = low;
+    low = max(0, low - 8);
+    const uint32_t digits = (1u << (above - low)) - 1u;
     for (int i = tid; i < held; i += kThreads) {
       const uint32_t key = s_key[i];
-      if (pass == 0 || (key >> (low + 8)) == prefix) atomicAdd(&s_hist[pass][(key >> low) & 255u], 1u);
+      if (key != kAlways && (above == 32 || (key >> above) == prefix)) atomicAdd(&s_hist[(key >> low) & digits], 1u);
     }
     __syncthreads();
     // thread b: keys in bin 255 - b; inclusive sums from the top
-    const uint32_t c = s_hist[pass][255 - tid];
+    const uint32_t c = s_hist[255 - tid];
     uint32_t up = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -203,45 +220,68 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     }
     if (lane == 31) s_warp[warp] = up;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) up += s_warp[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (w < warp) up += s_warp[w];
     if (up >= (uint32_t)need && up - c < (uint32_t)need) s_pick[0] = 255 - tid, s_pick[1] = need - (up - c), s_pick[2] = c;
+    s_hist[255 - tid] = 0;
     __syncthreads();
-    prefix = (prefix << 8) | s_pick[0];
+    prefix = (above == 32 ? 0u : prefix << (above - low)) | s_pick[0];
     need = (int)s_pick[1];
     threshold = prefix << low;
-    if (low > 0 && s_pick[2] == (uint32_t)need) {  // the whole bin is taken (held > budget: threshold > 0)
-      threshold -= 1;
+    const uint32_t in_bin = s_pick[2];
+    if (low == 0) break;
+    if (in_bin == (uint32_t)need) {  // the whole bin is taken; a key below it exists, so threshold > 0
+      threshold -= 1u;
       need = 0;
+      break;
+    }
+    if (in_bin <= (uint32_t)kThreads) {  // rank the bin's keys: one for each thread
+      for (int i = tid; i < held; i += kThreads) {
+        const uint32_t key = s_key[i];
+        if (key != kAlways && (key >> low) == prefix) s_bin[atomicAdd(&s_found, 1u)] = key;
+      }
+      __syncthreads();
+      if (tid < (int)in_bin) {
+        const uint32_t key = s_bin[tid];
+        uint32_t more = 0, same = 0;
+        for (uint32_t i = 0; i < in_bin; ++i) more += s_bin[i] > key, same += s_bin[i] == key;
+        // equal keys write the same two numbers
+        if (more < (uint32_t)need && more + same >= (uint32_t)need) s_pick[0] = key, s_pick[1] = need - more;
+      }
+      __syncthreads();
+      threshold = s_pick[0];
+      need = (int)s_pick[1];
       break;
     }
   }
 
-  // every key above the threshold and the first `need` equal to it, a stretch of pages for each thread
-  const int stretch = (held + kThreads - 1) / kThreads;
-  const int i0 = min(tid * stretch, held), i1 = min(i0 + stretch, held);
-  uint32_t mine = 0;  // keys above (high half) and equal (low half): at most kMaxPages of each
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t key = s_key[i];
-    mine += key > threshold ? 0x10000u : (key == threshold ? 1u : 0u);
-  }
-  uint32_t up = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
-    if (lane >= o) up += x;
+  // every key above the threshold and the first `need` equal to it, in order: a
+  // stretch of pages for each warp
+  const int stretch = ((held + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = min(warp * stretch, held), w1 = min(w0 + stretch, held);
+  uint32_t above = 0, equal = 0;
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t key = i + lane < w1 ? s_key[i + lane] : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key > threshold));
+    equal += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key == threshold));
   }
   __syncthreads();  // s_warp of the last pass is read
-  if (lane == 31) s_warp[warp] = up;
+  if (lane == 0) s_warp[warp] = above, s_warp2[warp] = equal;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) up += s_warp[w];
-  up -= mine;
-  uint32_t above = up >> 16, equal = up & 0xffffu;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t key = s_key[i];
-    if (key > threshold || (key == threshold && equal < (uint32_t)need))
-      out[above + min(equal, (uint32_t)need)] = i;
-    above += key > threshold;
-    equal += key == threshold;
+  above = equal = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) above += s_warp[w], equal += s_warp2[w];
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t key = i + lane < w1 ? s_key[i + lane] : 0u;
+    const bool gt = i + lane < w1 && key > threshold, eq = i + lane < w1 && key == threshold;
+    const uint32_t gts = __ballot_sync(0xffffffffu, gt), eqs = __ballot_sync(0xffffffffu, eq);
+    const uint32_t eq_at = equal + __popc(eqs & below);
+    if (gt || (eq && eq_at < (uint32_t)need)) out[above + __popc(gts & below) + min(eq_at, (uint32_t)need)] = i + lane;
+    above += __popc(gts);
+    equal += __popc(eqs);
   }
 }
 
