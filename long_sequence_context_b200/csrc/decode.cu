@@ -16,6 +16,8 @@
 #include "cpattn.h"
 #include "kernels.h"
 #include "paged.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
 
 namespace cpattn {
 namespace {
@@ -24,6 +26,7 @@ using namespace paged;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr float kNothing = -3.0e38f;  // the running maximum before any key: finite, so that no difference is inf - inf
 constexpr int kChunk = 16;   // keys of one tile; never straddles pages
 constexpr int kPairCost = 4;  // what starting and finishing a pair costs, in units of keys
 constexpr int kMaxGroup = 64;
@@ -33,7 +36,8 @@ struct DecodeArgs {
   const int32_t *table, *lens, *pages;
   void* o;
   float *lse, *part_o, *part_ml;
-  int4* tail;
+  int4* tail;  // notes for the join: {request, kv head, last block, first block} or {-1}
+  int by_pair;  // one note for each pair (fewer pairs than blocks), else one for each block
   const float* kv_amax;
   unsigned* err;
   int R, Hq, Hkv, group, shift, max_pages, num_pages, budget;
@@ -64,6 +68,13 @@ __device__ __forceinline__ int request_units(const DecodeArgs& a, int len) {
 // Length of a pair on the line: its units and what a pair costs by itself.
 __device__ __forceinline__ int pair_weight(int units) { return units == 0 ? 0 : units + kPairCost; }
 
+// 2^x, 0 below 2^-126
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void store_o(const DecodeArgs& a, size_t i, float x) {
   if (a.o_bf16)
     static_cast<__nv_bfloat16*>(a.o)[i] = __float2bfloat16_rn(x);
@@ -71,58 +82,67 @@ __device__ __forceinline__ void store_o(const DecodeArgs& a, size_t i, float x) 
     static_cast<float*>(a.o)[i] = x;
 }
 
-// One warp's view of 16 keys.  Lane 4g + t holds, for every 8 heads, the scores
-// of keys g and g + 8 with heads 2t and 2t + 1, and of the output 8 columns for
-// every 64 (col()) of the same two heads: the accumulator layout of mma.m16n8k16
-// with the keys (scores) or the columns (output) as its 16 rows.
+// One warp's view of 16 keys in shared memory.  Lane 4g + t holds, for every 8
+// heads, the scores of two keys (slots g and g + 8) with heads 2t and 2t + 1, and
+// of the output 8 columns for every 64 (col()) of the same two heads: the
+// accumulator layout of mma.m16n8k16 with the keys (scores) or the columns
+// (output) as its 16 rows.
 //
+// The 16 rows of K, and those of V, are one contiguous block of the cache.  TMA
+// brings it as lines of 128 bytes whose 16-byte pieces are permuted (piece p of
+// line i stands at p ^ (i & 7)), and the lanes' order of keys and columns, which
+// both products leave free, is chosen per type so that the pieces a quarter of a
+// warp reads fall into different banks.
+__device__ __forceinline__ const char* piece(const char* block, int line, int p) {
+  return block + line * 128 + ((p ^ (line & 7)) << 4);
+}
+
 // FmaTile: fp32 caches, fp32 arithmetic throughout.
 template <int D, int NT>
 struct FmaTile {
   using CT = float;
   static constexpr int kQueryBytes = D * 4;  // shared memory of one head's query
   static constexpr float kLift = 0.f, kSlack = 8.f;
-  static constexpr int kCtas = NT == 1 ? 3 : 2;  // blocks of an SM
-  static constexpr int kSub = 1;
-  static constexpr int kVecs = D / 16;  // 16-byte loads of a lane's quarter of a row
-
-  float4 k[2][kVecs];
-  const float* v_rows;
+  static constexpr int kSub = 1;    // blocks of 16 keys a warp takes at a time
+  static constexpr int kDepth = 2;  // and how many times that it has under way
+  static constexpr int kCtas = D == 128 ? 1 : (NT == 1 ? 3 : 2);  // thread blocks of an SM
+  static constexpr int kLines = D / 32;                            // lines of a row
 
   __device__ static __forceinline__ int col(int h, int g, int e) { return 64 * h + 8 * g + e; }
+  __device__ static __forceinline__ int key_of(int slot) { return slot; }
+  // piece v of lane t's quarter of a line (two of eight)
+  __device__ static __forceinline__ int quarter(int t, int v) {
+    return kLines == 4 ? t + 4 * v : (t & 1) + 4 * (t >> 1) + 2 * v;
+  }
 
-  // the queries of `heads` heads from row `at` of q on, for all tiles of this block
+  // the queries of `heads` heads from row `at` of q on, for all warps of this block
   __device__ static __forceinline__ void stage_queries(char* s, float*, const void* q, size_t at, int group, int heads) {
     for (int i = threadIdx.x; i < heads * D; i += kThreads)
       reinterpret_cast<float*>(s)[i] = i / D < group ? static_cast<const float*>(q)[at * D + i] : 0.f;
   }
 
-  __device__ __forceinline__ void load_k(const CT* p) {
+  __device__ static __forceinline__ void scores(const char* k, const char* s_q, float (&s)[NT][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j)
-        k[r][j] = __ldg(reinterpret_cast<const float4*>(p + (g + 8 * r) * D + (j * 4 + t) * 4));
-  }
-  __device__ __forceinline__ void load_v(const CT* p) { v_rows = p; }
-
-  __device__ __forceinline__ void scores(const char* s_q, float (&s)[NT][4]) const {
-    const int t = threadIdx.x & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float acc[2][8] = {};
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j)
+      for (int l = 0; l < kLines; ++l)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const float4 f = *reinterpret_cast<const float4*>(s_q + (size_t)(nt * 8 + n) * D * 4 + (j * 4 + t) * 16);
+        for (int v = 0; v < 2; ++v) {
+          float4 x[2];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            acc[r][n] = fmaf(f.x, k[r][j].x, acc[r][n]);
-            acc[r][n] = fmaf(f.y, k[r][j].y, acc[r][n]);
-            acc[r][n] = fmaf(f.z, k[r][j].z, acc[r][n]);
-            acc[r][n] = fmaf(f.w, k[r][j].w, acc[r][n]);
+          for (int r = 0; r < 2; ++r) x[r] = *reinterpret_cast<const float4*>(piece(k, (g + 8 * r) * kLines + l, quarter(t, v)));
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const float4 f = *reinterpret_cast<const float4*>(s_q + (nt * 8 + n) * D * 4 + l * 128 + quarter(t, v) * 16);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              acc[r][n] = fmaf(f.x, x[r].x, acc[r][n]);
+              acc[r][n] = fmaf(f.y, x[r].y, acc[r][n]);
+              acc[r][n] = fmaf(f.z, x[r].z, acc[r][n]);
+              acc[r][n] = fmaf(f.w, x[r].w, acc[r][n]);
+            }
           }
         }
       // sum over the quad; lane t is left with heads 2t and 2t + 1
@@ -144,24 +164,25 @@ struct FmaTile {
   }
 
   // acc += p v; n_valid: rows behind it hold anything and count as zero
-  __device__ __forceinline__ void output(const float (&p)[NT][4], int n_valid, float (&acc)[NT][D / 64][16]) const {
+  __device__ static __forceinline__ void output(const char* v, const float (&p)[NT][4], int n_valid,
+                                                float (&acc)[NT][D / 64][16]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
+#pragma unroll 4
     for (int kk = 0; kk < kChunk; ++kk) {
       float x[D / 64][8];
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
-          float4 u = __ldg(reinterpret_cast<const float4*>(v_rows + kk * D + 64 * h + 8 * g + e));
+          float4 u = *reinterpret_cast<const float4*>(piece(v, kk * kLines + 2 * h + (g >> 2), 2 * (g & 3) + e / 4));
           if (kk >= n_valid) u = make_float4(0.f, 0.f, 0.f, 0.f);
           x[h][e] = u.x, x[h][e + 1] = u.y, x[h][e + 2] = u.z, x[h][e + 3] = u.w;
         }
       const int src_lane = (kk & 7) * 4 + t;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float p0 = __shfl_sync(0xffffffffu, p[nt][(kk >> 3) * 2], src_lane);
-        const float p1 = __shfl_sync(0xffffffffu, p[nt][(kk >> 3) * 2 + 1], src_lane);
+        const float p0 = __shfl_sync(0xffffffffu, kk < 8 ? p[nt][0] : p[nt][2], src_lane);
+        const float p1 = __shfl_sync(0xffffffffu, kk < 8 ? p[nt][1] : p[nt][3], src_lane);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
 #pragma unroll
@@ -193,51 +214,45 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Loads whose place in the instruction stream is fixed: left to itself the
-// compiler sinks a prefetch to its use and waits for each load in turn.
-__device__ __forceinline__ void load16(const char* p, uint32_t* w) {
-  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "l"(p));
-}
-__device__ __forceinline__ void load8(const char* p, uint32_t* w) {
-  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-}
-
 // MmaTile: bf16 and e4m3 caches on the tensor cores, S^T = K Q^T and O^T = V^T P^T
 // with up to 8 heads as the narrow side, so that a group of few heads wastes
-// little.  K and V go from global memory straight into the operand registers:
-// the contraction index of a product and the row index of O^T may be permuted
-// at will, so a lane's 16-byte load of consecutive columns is at once its share
-// of one or more operands, and no shared memory, no wait and no barrier stands
-// between memory and the tensor cores.  8-bit codes are widened to half
-// precision, which holds them exactly; the queries then are in half precision
-// too, scaled per head by a power of two so that none of their bits is lost.
-// The weights enter as the sum of two 16-bit numbers (2^-17 relative or
-// better): the kernel waits for memory, the second product is free, and fp32
-// outputs stay good to that.
+// little.  A lane's 16 bytes of consecutive columns are at once its share of one
+// or more operands (the contraction index may be permuted at will).  8-bit codes
+// are widened to half precision, which holds them exactly; the queries then are
+// in half precision too, scaled per head by a power of two so that none of their
+// bits is lost.  The weights enter as the sum of two 16-bit numbers (2^-17
+// relative or better): the kernel waits for memory, the second product is free,
+// and fp32 outputs stay good to that.
 template <typename C, int D, int NT>
 struct MmaTile {
   using CT = C;
   static constexpr bool kHalf = sizeof(C) == 1;
   static constexpr int kQueryBytes = D * 2;
+  static constexpr int kRowBytes = D * (int)sizeof(C);  // 256, 128 or 64
+  static constexpr int kSub = 256 / kRowBytes;          // 8 KB of K and V at a time, 16 under way
+  static constexpr int kDepth = 2;
   static constexpr int kCtas = NT == 1 ? 3 : 2;
-  static constexpr int kSub = NT == 1 ? 256 / (D * (int)sizeof(C)) : 1;  // 4 KB of keys at a time
   // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
   // ends at 2^-24, which must be far below the largest weight of a long context.
   static constexpr float kLift = kHalf ? 14.f : 0.f, kSlack = kHalf ? 1.f : 8.f;
-  static constexpr int kRowVecs = D * (int)sizeof(C) / 64;  // 16-byte loads of a lane's quarter of a key
-  static constexpr int kVWords = D * (int)sizeof(C) / 32;   // words of a lane's eighth of a value row
-
-  uint32_t k[2][kRowVecs * 4];
-  uint32_t v[4][kVWords];
 
   __device__ static __forceinline__ int col(int h, int g, int e) {
     return kHalf ? D / 8 * g + 8 * h + e : 64 * h + 8 * g + e;
   }
-  // the 8 columns that lane t's part of query entry e stands for
+  // The key of a row slot.  Rows of 256 bytes are two lines: keys 2t and 2t + 8 of the
+  // natural order would share banks.
+  __device__ static __forceinline__ int key_of(int slot) {
+    if constexpr (kRowBytes == 256)
+      return (slot & 8) + ((slot & 1) ? 4 + (((slot & 7) / 2 + 1) & 3) : (slot & 7) / 2);
+    else
+      return slot;
+  }
+  // the 8 columns of lane t's part of query entry e (a quarter of a row is D / 32 entries)
   __device__ static __forceinline__ int query_col(int e, int t) {
-    return kHalf ? 64 * (e >> 1) + 16 * t + 8 * (e & 1) : 32 * e + 8 * t;
+    if constexpr (kRowBytes == 256) return 64 * (e >> 1) + 8 * ((t & 1) + 4 * (t >> 1) + 2 * (e & 1));
+    if constexpr (kHalf && D == 128) return 16 * (2 * t + (e >> 1)) + 8 * (e & 1);
+    if constexpr (kHalf) return 16 * t + 8 * e;
+    return 8 * (2 * t + e);
   }
 
   // s: [head / 8][entry][lane] 16 bytes, lane 4 * (head % 8) + t; unit[head]: what a score is multiplied by
@@ -285,49 +300,40 @@ struct MmaTile {
     }
   }
 
-  __device__ __forceinline__ void load_k(const CT* p) {
+  __device__ static __forceinline__ void scores(const char* k, const char* s_q, float (&s)[NT][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int j = 0; j < kRowVecs; ++j)
-        load16(reinterpret_cast<const char*>(p) + (g + 8 * r) * D * (int)sizeof(CT) + j * 64 + t * 16, &k[r][4 * j]);
-  }
-  __device__ __forceinline__ void load_v(const CT* p) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = 2 * t + (i & 1) + 8 * (i >> 1);
-      const char* row = reinterpret_cast<const char*>(p) + key * D * (int)sizeof(CT);
-      if constexpr (kVWords == 2) {
-        load8(row + g * 8, v[i]);
-      } else {
-#pragma unroll
-        for (int h = 0; h < kVWords / 4; ++h) load16(row + h * 128 + g * 16, &v[i][4 * h]);
-      }
-    }
-  }
-
-  __device__ __forceinline__ void scores(const char* s_q, float (&s)[NT][4]) const {
-    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+    uint32_t w[2][kRowBytes / 16];  // the lane's quarters of rows g, g + 8
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int key = key_of(g + 8 * r);
+#pragma unroll
+      for (int j = 0; j < kRowBytes / 64; ++j) {
+        int line, p;
+        if constexpr (kRowBytes == 256) line = 2 * key + (j >> 1), p = (t & 1) + 4 * (t >> 1) + 2 * (j & 1);
+        else if constexpr (kRowBytes == 128) line = key, p = 2 * t + j;
+        else line = key >> 1, p = 4 * (key & 1) + t;
+        const uint4 u = *reinterpret_cast<const uint4*>(piece(k, line, p));
+        w[r][4 * j] = u.x, w[r][4 * j + 1] = u.y, w[r][4 * j + 2] = u.z, w[r][4 * j + 3] = u.w;
+      }
+    }
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {
-      uint32_t a[2][4];  // rows g, g + 8: the operands of two steps of 16 columns
+      uint32_t a[2][4];  // the operands of two steps of 16 columns
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         if constexpr (kHalf) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            a[r][2 * i] = e4m3x2_to_half2((uint16_t)(k[r][2 * e + i] & 0xffffu));
-            a[r][2 * i + 1] = e4m3x2_to_half2((uint16_t)(k[r][2 * e + i] >> 16));
+            a[r][2 * i] = e4m3x2_to_half2((uint16_t)(w[r][2 * e + i] & 0xffffu));
+            a[r][2 * i + 1] = e4m3x2_to_half2((uint16_t)(w[r][2 * e + i] >> 16));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[r][i] = k[r][4 * e + i];
+          for (int i = 0; i < 4; ++i) a[r][i] = w[r][4 * e + i];
         }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -352,14 +358,31 @@ struct MmaTile {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
 
-  __device__ __forceinline__ void output(const float (&p)[NT][4], int n_valid, float (&acc)[NT][D / 64][16]) {
-    const int t = threadIdx.x & 3;
+  __device__ static __forceinline__ void output(const char* block, const float (&p)[NT][4], int n_valid,
+                                                float (&acc)[NT][D / 64][16]) {
+    constexpr int kWords = kRowBytes / 32;  // of a lane's eighth of a row
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint32_t v[4][kWords];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = key_of(2 * t + (i & 1) + 8 * (i >> 1));
+      if constexpr (kWords == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(piece(block, key >> 1, 4 * (key & 1) + (g >> 1)) + 8 * (g & 1));
+        v[i][0] = u.x, v[i][1] = u.y;
+      } else {
+#pragma unroll
+        for (int h = 0; h < kWords / 4; ++h) {
+          const uint4 u = *reinterpret_cast<const uint4*>(piece(block, key * (kWords / 4) + h, g));
+          v[i][4 * h] = u.x, v[i][4 * h + 1] = u.y, v[i][4 * h + 2] = u.z, v[i][4 * h + 3] = u.w;
+        }
+      }
+    }
     if (n_valid < kChunk) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (2 * t + (i & 1) + 8 * (i >> 1) >= n_valid)
+        if (key_of(2 * t + (i & 1) + 8 * (i >> 1)) >= n_valid)
 #pragma unroll
-          for (int w = 0; w < kVWords; ++w) v[i][w] = 0u;
+          for (int w = 0; w < kWords; ++w) v[i][w] = 0u;
     }
     uint32_t b[NT][2][2];  // [head tile][high, low part][keys 0-7, 8-15]
 #pragma unroll
@@ -375,18 +398,18 @@ struct MmaTile {
     for (int h = 0; h < D / 64; ++h)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        uint32_t w[4];  // columns col(h, g, 2m), + 1 of the lane's four keys
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (kHalf) {
-            const uint32_t x = v[i][2 * h + (m >> 1)];
-            w[i] = e4m3x2_to_half2((uint16_t)((m & 1) ? x >> 16 : x & 0xffffu));
-          } else {
-            w[i] = v[i][4 * h + m];
-          }
+        // columns col(h, g, 2m) (a0, a2) and the next (a1, a3) of the lane's key pairs
+        uint32_t a0, a1, a2, a3;
+        if constexpr (kHalf) {
+          const int w = 2 * h + (m >> 1);
+          const uint32_t x = __byte_perm(v[0][w], v[1][w], (m & 1) ? 0x7362 : 0x5140);
+          const uint32_t y = __byte_perm(v[2][w], v[3][w], (m & 1) ? 0x7362 : 0x5140);
+          a0 = e4m3x2_to_half2((uint16_t)(x & 0xffffu)), a1 = e4m3x2_to_half2((uint16_t)(x >> 16));
+          a2 = e4m3x2_to_half2((uint16_t)(y & 0xffffu)), a3 = e4m3x2_to_half2((uint16_t)(y >> 16));
+        } else {
+          a0 = __byte_perm(v[0][4 * h + m], v[1][4 * h + m], 0x5410), a1 = __byte_perm(v[0][4 * h + m], v[1][4 * h + m], 0x7632);
+          a2 = __byte_perm(v[2][4 * h + m], v[3][4 * h + m], 0x5410), a3 = __byte_perm(v[2][4 * h + m], v[3][4 * h + m], 0x7632);
         }
-        const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
-        const uint32_t a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_16816(kHalf, &acc[nt][h][4 * m], a0, a1, a2, a3, b[nt][0][0], b[nt][0][1]);
@@ -397,25 +420,43 @@ struct MmaTile {
 };
 
 template <typename Tile, int D, int NT>
-__global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, Tile::kCtas)
+    decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using CT = typename Tile::CT;
-  constexpr int HT = 8 * NT;                           // heads of one warp
-  __shared__ __align__(16) float s_buf[kWarps * HT][D];  // the queries; then the warps' outputs
-  __shared__ float s_unit[kWarps * HT];
+  constexpr int HT = 8 * NT;                              // heads of one warp
+  constexpr int kGroups = NT == 1 ? 1 : kMaxGroup / HT;   // head groups at most
+  constexpr int kBlock = kChunk * D * (int)sizeof(CT);    // bytes of K (and of V) of 16 keys
+  constexpr int SUB = Tile::kSub, kDepth = Tile::kDepth;
+  constexpr int UNIT = kWarps * SUB * kChunk;             // keys of one unit
+  // the warps' rings of K and V blocks; between pairs, when nothing is under way, the warps' outputs
+  extern __shared__ char s_raw[];
+  char* s_ring = s_raw + ((1024u - (sm100::smem_u32(s_raw) & 1023u)) & 1023u);
+  float(*s_buf)[D] = reinterpret_cast<float(*)[D]>(s_ring);
+  __shared__ __align__(16) char s_queries[kGroups * HT * Tile::kQueryBytes];
+  __shared__ __align__(8) uint64_t s_full[kWarps][kDepth];
+  __shared__ int s_valid[kWarps][kDepth][SUB], s_abort;
+  __shared__ float s_unit[kGroups * HT];
   __shared__ float s_m[kWarps][HT], s_l[kWarps][HT];
   __shared__ long long s_scan[kWarps], s_base;
   __shared__ int s_r;
 
-  constexpr int SUB = Tile::kSub;                // tiles a warp takes at a time
-  constexpr int UNIT = kWarps * SUB * kChunk;    // keys of one unit
-
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its places
+  if (tid == 0) {
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kDepth; ++i) sm100::mbar_init(&s_full[w][i], SUB);
+    s_abort = 0;
+    sm100::fence_barrier_init();
+    sm100::prefetch_tensormap(&k_map);
+    sm100::prefetch_tensormap(&v_map);
+  }
 
   // requests without a key: o = 0, lse = -inf
   for (int r = cta; r < a.R; r += gridDim.x) {
     if (request_units<UNIT>(a, request_len(a, r, tid == 0)) != 0) continue;
+    if (a.by_pair)
+      for (int h = tid; h < a.Hkv; h += kThreads) a.tail[r * a.Hkv + h] = make_int4(-1, 0, 0, 0);
     for (int i = tid; i < a.Hq * D; i += kThreads) store_o(a, (size_t)r * a.Hq * D + i, 0.f);
     for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)r * a.Hq + i] = -INFINITY;
   }
@@ -444,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
   long long u = 0, u_end = 0;
   if (cta < n_cta) u = total * cta / n_cta, u_end = total * (cta + 1) / n_cta;
   if (u >= u_end) {
-    if (tid == 0) a.tail[cta] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !a.by_pair) a.tail[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
   if (upto - mine <= u && u < upto) {  // one thread's requests hold the first unit
@@ -469,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
       sizeof(CT) == 1 ? a.scale_log2 / e4m3_scale(a.kv_amax) : a.scale_log2;
   const float v_unit = sizeof(CT) == 1 ? __fdiv_rn(1.f, e4m3_scale(a.kv_amax + 1)) : 1.f;
   int4 tail = make_int4(-1, 0, 0, 0);
+  unsigned issued = 0, done = 0;  // blocks this warp has asked for and used
 
   while (u < u_end) {
     const int len = request_len(a, r, false);
@@ -484,12 +526,61 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
     // the pair's own cost stands before its units
     const int x0 = max(0, y0 - kPairCost), x1 = max(0, y1 - kPairCost);
     if (x0 == x1) continue;
-    const int n_list = listed_pages(a, len);
+    const int n_list = listed_pages(a, len), held = (int)(((unsigned)len + (1u << a.shift) - 1u) >> a.shift);
     const int32_t* table = a.table + (size_t)r * a.max_pages;
     const int32_t* list = a.pages ? a.pages + ((size_t)r * a.Hkv + h) * a.budget : nullptr;
 
-    __syncthreads();  // the previous pair's queries and partial outputs are read
-    Tile::stage_queries(reinterpret_cast<char*>(s_buf), s_unit, a.q, (size_t)r * a.Hq + (size_t)h * a.group, a.group,
+    // The warps take the pair's blocks of 16 keys in turn, SUB at a time: this warp's
+    // i-th turn are blocks (first + i * kwarps) * SUB and the next ones.  Each lane
+    // knows where one of the next 32 blocks stands and asks for it when its turn is
+    // kDepth away; the pages of the 32 after them are read half way.  Blocks that are
+    // not there (behind the end, padding of the list, a page out of range) pass
+    // through the ring empty.
+    const int first = x0 * kWarps + kw, n_mine = (x1 * kWarps - first + kwarps - 1) / kwarps;
+    constexpr int kTurns = 32 / SUB;  // whose blocks the lanes hold
+    int line = 0, valid = 0, line_next = 0, valid_next = 0;
+    auto look = [&](int turn0) {  // of the turns from turn0 on
+      const int i = turn0 + lane / SUB;
+      const unsigned at = ((unsigned)(first + i * kwarps) * SUB + lane % SUB) * kChunk;
+      const int j = (int)(at >> a.shift), off = (int)(at & ((1u << a.shift) - 1u));
+      valid_next = 0;
+      if (i < n_mine && j < n_list) {
+        const int logical = list ? list[j] : j;
+        if ((unsigned)logical < (unsigned)held) {  // neither padding nor behind the end
+          const int page = table[logical];
+          valid_next = max(0, min(kChunk, len - ((logical << a.shift) + off)));
+          if (valid_next > 0 && (unsigned)page >= (unsigned)a.num_pages) {
+            atomicOr(a.err, kErrPage);
+            valid_next = 0;
+          }
+          line_next = (int)(((((long long)page * a.Hkv + h) << a.shift) + off) * (D * (int)sizeof(CT)) / 128);
+        }
+      }
+    };
+    auto issue = [&](int i) {
+      if (i % kTurns == 0) line = line_next, valid = valid_next;
+      if (i % kTurns == kTurns / 2 && i / kTurns * kTurns + kTurns < n_mine) look(i / kTurns * kTurns + kTurns);
+      if (lane / SUB == i % kTurns) {
+        const int slot = (int)(issued % kDepth), sub = lane % SUB;
+        char* to = s_ring + ((warp * kDepth + slot) * SUB + sub) * 2 * kBlock;
+        s_valid[warp][slot][sub] = valid;
+        if (valid > 0 && !s_abort) {
+          sm100::mbar_expect_tx(&s_full[warp][slot], 2 * kBlock);
+          sm100::tma_load_2d(to, &k_map, &s_full[warp][slot], 0, line);
+          sm100::tma_load_2d(to + kBlock, &v_map, &s_full[warp][slot], 0, line);
+        } else {
+          sm100::mbar_arrive(&s_full[warp][slot]);
+        }
+      }
+      ++issued;
+    };
+
+    // the previous pair's outputs were written and read where the copies go now
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    look(0);
+    for (int i = 0; i < min(kDepth, n_mine); ++i) issue(i);
+    Tile::stage_queries(s_queries, s_unit, a.q, (size_t)r * a.Hq + (size_t)h * a.group, a.group,
                         hgroups * HT);
     __syncthreads();
 
@@ -497,14 +588,14 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[nt][i] = -INFINITY, l[nt][i] = 0.f;
+      for (int i = 0; i < 2; ++i) m[nt][i] = kNothing, l[nt][i] = 0.f;
 #pragma unroll
       for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[nt][hh][e] = 0.f;
     }
 
-    const char* s_q = reinterpret_cast<const char*>(s_buf) + hg * HT * Tile::kQueryBytes;
+    const char* s_q = s_queries + hg * HT * Tile::kQueryBytes;
     float unit[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -512,101 +603,80 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
       for (int i = 0; i < 2; ++i)
         unit[nt][i] = scale_log2 * (sizeof(CT) == 1 ? s_unit[hg * HT + nt * 8 + 2 * t + i] : 1.f);
 
-    // Tile c of the pair: its first row in the cache and how many of its 16 keys
-    // count; tiles that are not there read row 0 and count none.
-    const int c_end = x1 * kWarps * SUB;
-    auto locate = [&](int c, int& n_valid) -> size_t {
-      n_valid = 0;
-      const int j = (int)((unsigned)c * kChunk >> a.shift);
-      if (c >= c_end || j >= n_list) return 0;
-      const int off = (int)((unsigned)c * kChunk) & ((1 << a.shift) - 1);
-      const int logical = list ? list[j] : j;
-      const long long pos = ((long long)logical << a.shift) + off;
-      if (logical < 0 || pos >= len) return 0;  // padding of the list, or behind the end
-      const int page = table[logical];
-      if (page < 0 || page >= a.num_pages) {
-        if (lane == 0) atomicOr(a.err, kErrPage);
-        return 0;
+    for (int i = 0; i < n_mine; ++i, ++done) {
+      const int slot = (int)(done % kDepth);
+      if (!sm100::mbar_wait_warp(&s_full[warp][slot], (uint32_t)(done / kDepth) & 1u, &s_abort, a.err)) break;
+      const char* block = s_ring + (warp * kDepth + slot) * SUB * 2 * kBlock;
+      int n_valid[SUB], least = kChunk;
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub) {
+        n_valid[sub] = s_valid[warp][slot][sub];
+        least = min(least, n_valid[sub]);
       }
-      n_valid = (int)min((long long)kChunk, len - pos);
-      return ((((size_t)page * a.Hkv + h) << a.shift) + off) * D;
-    };
-
-    // The next tiles' K is on its way while these ones' softmax and output run;
-    // where they stand is known one step earlier still.
-    Tile tile[SUB];
-    const CT* kc = static_cast<const CT*>(a.k);
-    const CT* vc = static_cast<const CT*>(a.v);
-    const int step = kwarps * SUB;
-    int c = x0 * kWarps * SUB + kw * SUB, n_valid[SUB], n_next[SUB];
-    size_t row[SUB], row_next[SUB];
-#pragma unroll
-    for (int i = 0; i < SUB; ++i) row[i] = locate(c + i, n_valid[i]);
-#pragma unroll
-    for (int i = 0; i < SUB; ++i) row_next[i] = locate(c + step + i, n_next[i]);
-    if (c < c_end)
-#pragma unroll
-      for (int i = 0; i < SUB; ++i) tile[i].load_k(kc + row[i]);
-    for (; c < c_end; c += step) {
       float s[SUB][NT][4];
 #pragma unroll
-      for (int i = 0; i < SUB; ++i) tile[i].load_v(vc + row[i]);
-#pragma unroll
-      for (int i = 0; i < SUB; ++i) tile[i].scores(s_q, s[i]);
-      if (c + step < c_end)
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) tile[i].load_k(kc + row_next[i]);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float mx[2] = {-INFINITY, -INFINITY};
+      for (int sub = 0; sub < SUB; ++sub) Tile::scores(block + sub * 2 * kBlock, s_q, s[sub]);
+      if (least < kChunk) {
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float& x = s[sub][nt][i];
-            x = (g + 8 * (i >> 1)) < n_valid[sub] ? x * unit[nt][i & 1] : -INFINITY;
-            mx[i & 1] = fmaxf(mx[i & 1], x);
-          }
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int e = 0; e < 4; ++e)
+              if (Tile::key_of(g + 8 * (e >> 1)) >= n_valid[sub]) s[sub][nt][e] = -INFINITY;
+      }
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-        // the reference of the weights follows the maximum only when that has grown by kSlack
+      for (int nt = 0; nt < NT; ++nt) {
+        // unit > 0: the largest product is the largest score
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+#pragma unroll
+          for (int sub = 1; sub < SUB; ++sub) mx[e] = fmaxf(mx[e], fmaxf(s[sub][nt][e], s[sub][nt][e + 2]));
+          mx[e] *= unit[nt][e];
+        }
+        // The reference of the weights follows the largest score only when that has grown by
+        // kSlack; a lane looks at its own keys first.
         if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + (Tile::kLift + Tile::kSlack) ||
                                         mx[1] > m[nt][1] + (Tile::kLift + Tile::kSlack))) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float mn = fmaxf(m[nt][i], mx[i] - Tile::kLift);
-            const float alpha = exp2f(m[nt][i] - (mn == -INFINITY ? 0.f : mn));
-            m[nt][i] = mn;
-            l[nt][i] *= alpha;
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+            const float mn = fmaxf(m[nt][e], mx[e] - Tile::kLift);
+            const float alpha = exp2_fast(m[nt][e] - mn);
+            m[nt][e] = mn;
+            l[nt][e] *= alpha;
 #pragma unroll
             for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) acc[nt][hh][2 * e + i] *= alpha;
+              for (int x = 0; x < 8; ++x) acc[nt][hh][2 * x + e] *= alpha;
           }
         }
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float b = m[nt][i & 1];
-            float& x = s[sub][nt][i];
-            x = exp2f(x - (b == -INFINITY ? 0.f : b));
-            l[nt][i & 1] += x;
+          for (int e = 0; e < 4; ++e) {
+            s[sub][nt][e] = exp2_fast(fmaf(s[sub][nt][e], unit[nt][e & 1], -m[nt][e & 1]));
+            l[nt][e & 1] += s[sub][nt][e];
           }
       }
 #pragma unroll
-      for (int i = 0; i < SUB; ++i) tile[i].output(s[i], n_valid[i], acc);
-      int n_after[SUB];
-      size_t row_after[SUB];
-#pragma unroll
-      for (int i = 0; i < SUB; ++i) row_after[i] = locate(c + 2 * step + i, n_after[i]);
-#pragma unroll
-      for (int i = 0; i < SUB; ++i) {
-        row[i] = row_next[i], n_valid[i] = n_next[i];
-        row_next[i] = row_after[i], n_next[i] = n_after[i];
+      for (int sub = 0; sub < SUB; ++sub)
+        Tile::output(block + sub * 2 * kBlock + kBlock, s[sub], n_valid[sub], acc);
+      __syncwarp();  // the block is read
+      if (i + kDepth < n_mine) issue(i + kDepth);
+    }
+    // After a wait that ran out nothing new is issued; what is under way is waited for, with the same limit.
+    if (s_abort) {
+      for (int i = 0; i < kDepth; ++i) {
+        const unsigned long long t0 = sm100::globaltimer();
+        while (i < issued - done && !sm100::mbar_try_wait(&s_full[warp][(done + i) % kDepth], (uint32_t)((done + i) / kDepth) & 1u) &&
+               sm100::globaltimer() - t0 < sm100::kWaitLimitNs) {
+        }
       }
+      done = issued;
     }
 
     // the warps' results side by side, then one per head
@@ -629,11 +699,10 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
     const int slot = 2 * cta + (x0 == 0 ? 1 : 0);
     for (int i = tid; i < a.group * D; i += kThreads) {
       const int head = i / D, d = i % D, hw = head / HT, hh = head % HT;
-      float mm = -INFINITY, ll = 0.f, oo = 0.f;
+      float mm = kNothing, ll = 0.f, oo = 0.f;
       for (int w = 0; w < kwarps; ++w) mm = fmaxf(mm, s_m[w * hgroups + hw][hh]);
-      const float b = mm == -INFINITY ? 0.f : mm;
       for (int w = 0; w < kwarps; ++w) {
-        const float f = exp2f(s_m[w * hgroups + hw][hh] - b);
+        const float f = exp2_fast(s_m[w * hgroups + hw][hh] - mm);
         ll = fmaf(f, s_l[w * hgroups + hw][hh], ll);
         oo = fmaf(f, s_buf[(w * hgroups + hw) * HT + hh][d], oo);
       }
@@ -641,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
       if (whole) {
         const size_t out = (size_t)r * a.Hq + (size_t)h * a.group + head;
         store_o(a, out * D + d, ll == 0.f ? 0.f : oo / ll);
-        if (d == 0) a.lse[out] = ll == 0.f ? -INFINITY : (b + log2f(ll)) * 0.69314718055994531f;
+        if (d == 0) a.lse[out] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
       } else {
         a.part_o[((size_t)slot * a.group + head) * D + d] = oo;
         if (d == 0) {
@@ -650,67 +719,88 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas) decode_kernel(const Dec
         }
       }
     }
-    if (!whole && x0 == 0) {
+    if (x0 == 0) {
       // the block that holds the pair's last unit: the largest c with total * c / n_cta <= last
       const long long last = base + (long long)(h + 1) * w_pair - 1;
-      tail = make_int4(r, h, (int)(((last + 1) * n_cta - 1) / total), 0);
+      if (!whole) tail = make_int4(r, h, (int)(((last + 1) * n_cta - 1) / total), cta);
+      if (tid == 0 && a.by_pair) a.tail[r * a.Hkv + h] = whole ? make_int4(-1, 0, 0, 0) : tail;
     }
   }
-  if (tid == 0) a.tail[cta] = tail;
+  if (tid == 0 && !a.by_pair) a.tail[cta] = tail;
 }
 
-// Combines the partial results of the pair that starts in block blockIdx.x and
-// continues in the following ones: M = max m_c, o = sum e^{m_c - M} o_c / sum
-// e^{m_c - M} l_c.  Four heads for each blockIdx.y, four warps for each head,
-// every fourth part for each warp.
-constexpr int kJoinHeads = 4, kJoinWays = 4, kJoinWarps = kJoinHeads * kJoinWays;
+// Combines the partial results of a pair that starts in one block and continues
+// in the following ones: M = max m_c, o = sum e^{m_c - M} o_c / sum e^{m_c - M} l_c.
+// Block x looks at the x-th note about such a pair, block y at a share of its
+// heads; `ways` warps take a head's parts in turn, eight loads at a time.
+constexpr int kJoinWarps = 16;  // at most
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs a, int ways) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 tail = a.tail[blockIdx.x];
   if (tail.x < 0) return;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int first = blockIdx.x, n_parts = tail.z - first + 1;
-  constexpr int V = D / 32;
-  const int head = blockIdx.y * kJoinHeads + warp / kJoinWays, way = warp % kJoinWays;
+  const int first = tail.w, n_parts = tail.z - first + 1;
+  constexpr int V = D / 32, kAhead = 8;
+  const int head = blockIdx.y * ((blockDim.x >> 5) / ways) + warp / ways, way = warp % ways;
   auto part = [&](int c) { return (size_t)(c == 0 ? 2 * first + 1 : 2 * (first + c)) * a.group + head; };
-  float m = -INFINITY, l = 0.f, o[V] = {};
+  float m = kNothing, l = 0.f, o[V] = {};
   if (head < a.group) {
-    for (int c = way + kJoinWays * lane; c < n_parts; c += kJoinWays * 32) m = fmaxf(m, a.part_ml[part(c) * 2]);
+    for (int c0 = way; c0 < n_parts; c0 += ways * kAhead) {
+      float pm[kAhead], pl[kAhead], po[kAhead][V];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const float b = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-    for (int c = way; c < n_parts; c += kJoinWays) {
-      const size_t at = part(c);
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-      const float f = exp2f(ml.x - b);
-      l = fmaf(f, ml.y, l);
+      for (int i = 0; i < kAhead; ++i) {
+        const int c = c0 + i * ways;
+        pm[i] = kNothing, pl[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = fmaf(f, a.part_o[at * D + e * 32 + lane], o[e]);
+        for (int e = 0; e < V; ++e) po[i][e] = 0.f;
+        if (c < n_parts) {
+          const size_t at = part(c);
+          asm volatile("ld.global.v2.f32 {%0,%1}, [%2];" : "=f"(pm[i]), "=f"(pl[i]) : "l"(a.part_ml + at * 2));
+          const float* from = a.part_o + at * D + lane * V;
+          if constexpr (V == 4)
+            asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(po[i][0]), "=f"(po[i][1]), "=f"(po[i][2]), "=f"(po[i][V - 1])
+                         : "l"(from));
+          else
+            asm volatile("ld.global.v2.f32 {%0,%1}, [%2];" : "=f"(po[i][0]), "=f"(po[i][V - 1]) : "l"(from));
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) mn = fmaxf(mn, pm[i]);
+      const float f0 = exp2_fast(m - mn);
+      m = mn;
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] *= f0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float f = exp2_fast(pm[i] - mn);
+        l = fmaf(f, pl[i], l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(f, po[i][e], o[e]);
+      }
     }
   }
 #pragma unroll
-  for (int e = 0; e < V; ++e) s_o[warp][e * 32 + lane] = o[e];
+  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = o[e];
   if (lane == 0) s_m[warp] = m, s_l[warp] = l;
   __syncthreads();
   if (way == 0 && head < a.group) {
-    float mm = -INFINITY, ll = 0.f, oo[V] = {};
-#pragma unroll
-    for (int w = 0; w < kJoinWays; ++w) mm = fmaxf(mm, s_m[warp + w]);
-    const float b = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-    for (int w = 0; w < kJoinWays; ++w) {
-      const float f = exp2f(s_m[warp + w] - b);
+    float mm = kNothing, ll = 0.f, oo[V] = {};
+    for (int w = 0; w < ways; ++w) mm = fmaxf(mm, s_m[warp + w]);
+    for (int w = 0; w < ways; ++w) {
+      const float f = exp2_fast(s_m[warp + w] - mm);
       ll = fmaf(f, s_l[warp + w], ll);
 #pragma unroll
-      for (int e = 0; e < V; ++e) oo[e] = fmaf(f, s_o[warp + w][e * 32 + lane], oo[e]);
+      for (int e = 0; e < V; ++e) oo[e] = fmaf(f, s_o[warp + w][lane * V + e], oo[e]);
     }
     const size_t out = (size_t)tail.x * a.Hq + (size_t)tail.y * a.group + head;
 #pragma unroll
-    for (int e = 0; e < V; ++e) store_o(a, out * D + e * 32 + lane, ll == 0.f ? 0.f : oo[e] / ll);
-    if (lane == 0) a.lse[out] = ll == 0.f ? -INFINITY : (b + log2f(ll)) * 0.69314718055994531f;
+    for (int e = 0; e < V; ++e) store_o(a, out * D + lane * V + e, ll == 0.f ? 0.f : oo[e] / ll);
+    if (lane == 0) a.lse[out] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
   }
 }
 
@@ -734,17 +824,31 @@ template <typename Tile, int D, int NT>
 int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
   static_assert(Tile::kCtas <= kMostCtas, "the workspace is sized for kMostCtas");
   const int grid = decode_grid(Tile::kCtas, max_units);
+  a.by_pair = (long long)a.R * a.Hkv < grid;
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float*>(ws + ws_part_o(grid, a.group, D));
   a.tail = reinterpret_cast<int4*>(ws + ws_part_o(grid, a.group, D) + ws_part_ml(grid, a.group));
+  CUtensorMap k_map, v_map;
+  constexpr int kBlock = kChunk * D * (int)sizeof(typename Tile::CT), kBytes = kWarps * Tile::kDepth * Tile::kSub * 2 * kBlock + 1024;
+  const uint64_t lines = ((uint64_t)a.num_pages * a.Hkv << a.shift) * (kBlock / kChunk) / 128;
+  static std::atomic<unsigned long long> done{0};
+  if (!make_tmap_u8_2d(&k_map, a.k, lines, 128, 128, kBlock / 128) || !make_tmap_u8_2d(&v_map, a.v, lines, 128, 128, kBlock / 128) ||
+      !smem_attr_once(decode_kernel<Tile, D, NT>, kBytes, done))
+    return -1;
   prof_begin(kKDecode, s);
-  decode_kernel<Tile, D, NT><<<grid, kThreads, 0, s>>>(a);
+  decode_kernel<Tile, D, NT><<<grid, kThreads, kBytes, s>>>(a, k_map, v_map);
   prof_end(kKDecode, s);
   if (cudaGetLastError() != cudaSuccess) return -1;
   // the join starts while the last blocks finish and waits for them on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (a.group + kJoinHeads - 1) / kJoinHeads);
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  // Few pairs can have many parts: a large block for each head.  Else blocks of
+  // which most find nothing to do, small and with more heads each.
+  const int notes = a.by_pair ? a.R * a.Hkv : grid, sms = decode_grid(1, 1LL << 40);
+  const int warps = (long long)notes * a.group <= sms ? kJoinWarps : kJoinWarps / 2;
+  int heads = 1;
+  while (heads < warps / 2 && (long long)notes * ((a.group + heads - 1) / heads) > 2LL * sms) heads *= 2;
+  cfg.gridDim = dim3(notes, (a.group + heads - 1) / heads);
+  cfg.blockDim = dim3(warps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -752,7 +856,7 @@ int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   prof_begin(kKDecodeJoin, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<D>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<D>, a, warps / heads);
   prof_end(kKDecodeJoin, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 2 : -1;
 }
@@ -800,6 +904,9 @@ int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,
   if (!sizes_ok(R, Hq, Hkv, D) || shift < 0 || max_pages < 1 || num_pages < 1) return CPATTN_ERR_SHAPE;
   if (((long long)max_pages << shift) > 0x7fffffffLL) return CPATTN_ERR_SHAPE;
   if ((long long)R * Hq * D > (1LL << 40)) return CPATTN_ERR_SHAPE;
+  // the kernel counts the cache's lines of 128 bytes in 31 bits (256 GB)
+  const long long row_bytes = (long long)D * (cache_dtype == CPATTN_FP32 ? 4 : cache_dtype == CPATTN_BF16 ? 2 : 1);
+  if ((long long)num_pages * Hkv > (1LL << 38) / row_bytes >> shift) return CPATTN_ERR_SHAPE;
   if (pages && budget < 1) return CPATTN_ERR_SHAPE;
   if (!q || !k_cache || !v_cache || !block_table || !lens || !o || !lse) return CPATTN_ERR_ARG;
   if (cache_dtype == CPATTN_E4M3 && !kv_amax) return CPATTN_ERR_ARG;
