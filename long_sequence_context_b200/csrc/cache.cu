@@ -178,16 +178,17 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
 __global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const PlanArgs a) {
   __shared__ int32_t s_at[3][kSmallR + 1], s_head[3];
   const Prefix p = {s_head, s_at[0], s_at[1], s_at[2]};
+  after_previous();
   plan_requests(a, p);
   __syncthreads();
   plan_items(a, p, threadIdx.x, blockDim.x);
 }
 __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();
   plan_requests(a, {a.head, a.cu, a.pop_at, a.push_at});
 }
 __global__ void __launch_bounds__(256) plan_items_kernel(const PlanArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   plan_items(a, {a.head, a.cu, a.pop_at, a.push_at}, (long long)blockIdx.x * blockDim.x + threadIdx.x,
              (long long)gridDim.x * blockDim.x);
 }
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   constexpr int V = 16 / (int)sizeof(IT);  // elements of a lane
   constexpr int kLanes = D / V, kRows = 32 / kLanes;  // lanes of a row, rows of a warp's load
   constexpr int kAhead = 4;
+  after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int page_mask = (1 << a.shift) - 1;
   const long long t0 = (long long)blockIdx.x * kTile;
@@ -363,12 +365,10 @@ int launch_append(const AppendArgs& a, int D, cudaStream_t s) {
   const long long share = std::max<long long>(1, std::min<long long>(65535, (warps + tiles * kAppendWarps - 1) / (tiles * kAppendWarps)));
   const dim3 grid((unsigned)tiles, (unsigned)share);
   prof_begin(kKCacheAppend, s);
-  if (D == 64)
-    append_kernel<IT, CT, 64><<<grid, kAppendWarps * 32, 0, s>>>(a);
-  else
-    append_kernel<IT, CT, 128><<<grid, kAppendWarps * 32, 0, s>>>(a);
+  const cudaError_t e = launch_chained(D == 64 ? append_kernel<IT, CT, 64> : append_kernel<IT, CT, 128>, grid,
+                                       kAppendWarps * 32, 0, 0, s, a);
   prof_end(kKCacheAppend, s);
-  return cudaGetLastError() == cudaSuccess ? 1 : -1;
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
 }  // namespace
@@ -431,30 +431,22 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!need) {
     prof_begin(kKCachePlan, s);
-    plan_small_kernel<<<1, kPlanThreads, 0, s>>>(a);
+    const cudaError_t e = launch_chained(plan_small_kernel, dim3(1), kPlanThreads, 0, 0, s, a);
     prof_end(kKCachePlan, s);
-    if (cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
+    if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
     add_launches(1);
     return CPATTN_OK;
   }
   int dev = 0;
   cudaGetDevice(&dev);
   prof_begin(kKCachePlan, s);
-  plan_requests_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  cudaError_t e = launch_chained(plan_requests_kernel, dim3(1), kPlanThreads, 0, 0, s, a);
   prof_end(kKCachePlan, s);
-  if (cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
+  if (e != cudaSuccess) return CPATTN_ERR_CUDA;
   const long long items = std::max<long long>(capacity, std::min<long long>((long long)R * max_pages, num_pages));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::max<long long>(1, std::min<long long>((items + 255) / 256, (long long)num_sms(dev) * 8)));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};  // the items' blocks take their places while the requests are summed, and wait
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  const unsigned blocks = (unsigned)std::max<long long>(1, std::min<long long>((items + 255) / 256, (long long)num_sms(dev) * 8));
   prof_begin(kKCachePlan, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_items_kernel, a);
+  e = launch_chained(plan_items_kernel, dim3(blocks), 256, 0, 0, s, a);
   prof_end(kKCachePlan, s);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
   add_launches(2);

@@ -442,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its places
   if (tid == 0) {
     for (int w = 0; w < kWarps; ++w)
       for (int i = 0; i < kDepth; ++i) sm100::mbar_init(&s_full[w][i], SUB);
@@ -451,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
     sm100::prefetch_tensormap(&k_map);
     sm100::prefetch_tensormap(&v_map);
   }
+  after_previous();
 
   // requests without a key: o = 0, lse = -inf
   for (int r = cta; r < a.R; r += gridDim.x) {
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
 constexpr int kJoinWarps = 16;  // at most
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs a, int ways) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const int4 tail = a.tail[blockIdx.x];
   if (tail.x < 0) return;
   __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
@@ -836,27 +836,17 @@ int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
       !smem_attr_once(decode_kernel<Tile, D, NT>, kBytes, done))
     return -1;
   prof_begin(kKDecode, s);
-  decode_kernel<Tile, D, NT><<<grid, kThreads, kBytes, s>>>(a, k_map, v_map);
+  cudaError_t e = launch_chained(decode_kernel<Tile, D, NT>, dim3(grid), kThreads, kBytes, 0, s, a, k_map, v_map);
   prof_end(kKDecode, s);
-  if (cudaGetLastError() != cudaSuccess) return -1;
-  // the join starts while the last blocks finish and waits for them on the device
-  cudaLaunchConfig_t cfg = {};
+  if (e != cudaSuccess) return -1;
   // Few pairs can have many parts: a large block for each head.  Else blocks of
   // which most find nothing to do, small and with more heads each.
   const int notes = a.by_pair ? a.R * a.Hkv : grid, sms = decode_grid(1, 1LL << 40);
   const int warps = (long long)notes * a.group <= sms ? kJoinWarps : kJoinWarps / 2;
   int heads = 1;
   while (heads < warps / 2 && (long long)notes * ((a.group + heads - 1) / heads) > 2LL * sms) heads *= 2;
-  cfg.gridDim = dim3(notes, (a.group + heads - 1) / heads);
-  cfg.blockDim = dim3(warps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   prof_begin(kKDecodeJoin, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<D>, a, warps / heads);
+  e = launch_chained(join_kernel<D>, dim3(notes, (a.group + heads - 1) / heads), warps * 32, 0, 0, s, a, warps / heads);
   prof_end(kKDecodeJoin, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 2 : -1;
 }

@@ -14,6 +14,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <utility>
+
 namespace cpattn {
 namespace paged {
 
@@ -36,6 +38,32 @@ inline int page_shift(int page_size) {
 
 inline bool aligned_to(const void* p, unsigned n) {
   return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+// One token's step is a chain of short kernels.  Each is launched so that it may
+// take its places while the kernel before it finishes, reads and writes nothing
+// before after_previous(), and only then lets the next one in.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                           cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 // 448 * (1 / amax), both steps rounded to fp32: what 448.0 / amax gives for a

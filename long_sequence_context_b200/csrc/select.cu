@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* out = a.sel + (size_t)pair * a.budget;
 
+  after_previous();
   const long long cap = (long long)a.max_pages << a.shift;
   long long len = a.lens[r];
   if (len < 0 || len > cap) {
@@ -295,19 +296,9 @@ int launch_dim(const SelectArgs& a, int cluster, cudaStream_t s) {
       cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return -1;
   if (!smem_attr_once(kernel, kMaxPages * (int)sizeof(uint32_t), done)) return -1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)a.R * a.Hkv * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.max_pages * sizeof(uint32_t);
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   prof_begin(kKSelect, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  const cudaError_t e = launch_chained(kernel, dim3((unsigned)((long long)a.R * a.Hkv * cluster)), kThreads,
+                                       a.max_pages * sizeof(uint32_t), cluster, s, a);
   prof_end(kKSelect, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
