@@ -1,23 +1,29 @@
-"""Build libcpattn.so (the C-ABI library) in-tree for sm_100a.
+"""Build libcpattn.so (the C-ABI library) in-tree for sm_100a, and _calls.so,
+the C++ side of the Python binding's per-token calls.
 
     python -m long_sequence_context_b200.build [--force] [--verbose]
 
 Each csrc/*.cu is compiled by nvcc (-gencode arch=compute_100a,code=sm_100a
 -O3 -lineinfo) into _build/, then linked into long_sequence_context_b200/
 libcpattn.so with the CUDA runtime linked statically.  No vendor math library
-is linked: every kernel is this package's own.
+is linked: every kernel is this package's own.  csrc/calls.cpp is host code
+against PyTorch's headers, compiled by g++.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcpattn.so")
+CALLS = os.path.join(PKG, "_calls.so")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -50,6 +56,22 @@ def _compile(src, verbose):
     return obj, (r.stdout + r.stderr)
 
 
+def _build_calls(force):
+    src = os.path.join(CSRC, "calls.cpp")
+    if not (force or _stale(CALLS, [src, os.path.join(ROOT, "include", "cpattn.h")])):
+        return
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(cuda, "include"),
+           "-I", sysconfig.get_paths()["include"], src, "-o", CALLS + ".tmp", "-L", os.path.join(torch_dir, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
@@ -69,6 +91,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_calls(force)
     if verbose:
         print("\n".join(logs))
     return LIB

@@ -91,6 +91,21 @@ def _load():
 lib = _load()
 
 
+def _load_calls():
+    try:
+        from long_sequence_context_b200 import _calls
+    except ImportError as e:
+        raise ImportError("_calls.so is missing or does not load: build it with "
+                          "`python -m long_sequence_context_b200.build`") from e
+    _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                  for n in ("cpattn_cache_plan_workspace_bytes", "cpattn_cache_plan", "cpattn_cache_append",
+                            "cpattn_select_pages", "cpattn_decode_workspace_bytes", "cpattn_decode")))
+    return _calls
+
+
+_calls = _load_calls()
+
+
 def status_str(status: int) -> str:
     return lib.cpattn_status_str(int(status)).decode()
 
@@ -481,15 +496,11 @@ def layer_bwd(x, w_qkv, w_o, saved, dy, num_heads: int, cp_size: int, causal: bo
 
 # ---- the paged key-value cache ----
 #
-# One token's step is a handful of calls of some microseconds each, and a check
-# by `_expect` takes about one: these calls compare everything in one expression
-# and look for the argument to name only when that fails.  (torch.empty takes
-# its sizes as separate arguments for the same reason.)
-
-def _fits(t, shape, dtype, dev) -> bool:
-    return isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.get_device() == dev \
-        and t.is_contiguous()
-
+# One token's step is a handful of calls of some microseconds each, and ctypes,
+# the checks and the outputs' allocation take as long: an ordinary call goes to
+# csrc/calls.cpp, which makes the same C calls.  What that declines (returns
+# None for) goes through the functions below: wrong arguments, which are named
+# here, and outputs, workspaces or streams that are given.
 
 def _cache(k_cache, v_cache, kv_amax):
     """Checks a paged cache; returns (its sizes, the rows' dtype, its dtype code, its device)."""
@@ -501,13 +512,11 @@ def _cache(k_cache, v_cache, kv_amax):
         raise ValueError(f"k_cache is empty: {tuple(shape)}")
     if not k_cache.is_contiguous():
         raise ValueError("k_cache must be contiguous")
-    if not _fits(v_cache, shape, dtype, dev):
-        _expect(v_cache, "v_cache", shape, dtype, k_cache)
+    _expect(v_cache, "v_cache", shape, dtype, k_cache)
     if code == E4M3:
         if kv_amax is None:
             raise ValueError("kv_amax must be given for an e4m3 (uint8) cache")
-        if not _fits(kv_amax, (2,), torch.float32, dev):
-            _expect(kv_amax, "kv_amax", (2,), torch.float32, k_cache)
+        _expect(kv_amax, "kv_amax", (2,), torch.float32, k_cache)
         return shape, torch.bfloat16, code, dev
     if kv_amax is not None:
         raise ValueError("kv_amax is for an e4m3 (uint8) cache only")
@@ -523,24 +532,15 @@ def _batch(block_table, lens, like=None):
     return block_table.shape
 
 
-def _queries(q, block_table, lens, dtype, heads, D, cache, dev):
+def _queries(q, block_table, lens, dtype, heads, D, cache):
     """Checks q [R, Hq, D] and the batch it belongs to against the cache; returns (R, Hq, max_pages)."""
-    try:
-        (R, max_pages), Hq = block_table.shape, q.shape[1]
-        right = (q.shape == (R, Hq, D) and lens.shape == (R,) and q.dtype is dtype
-                 and block_table.dtype is lens.dtype is torch.int32 and q.get_device() == dev
-                 and block_table.get_device() == dev and lens.get_device() == dev and q.is_contiguous()
-                 and block_table.is_contiguous() and lens.is_contiguous() and Hq % heads == 0)
-    except (AttributeError, TypeError, ValueError, IndexError):
-        right = False
-    if not right:
-        R, max_pages = _batch(block_table, lens, cache)
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must be a [R, Hq, D] tensor")
-        Hq = q.shape[1]
-        _expect(q, "q", (R, Hq, D), dtype, cache)
-        if Hq % heads != 0:
-            raise ValueError(f"q has {Hq} heads, not a multiple of the cache's {heads}")
+    R, max_pages = _batch(block_table, lens, cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [R, Hq, D] tensor")
+    Hq = q.shape[1]
+    _expect(q, "q", (R, Hq, D), dtype, cache)
+    if Hq % heads != 0:
+        raise ValueError(f"q has {Hq} heads, not a multiple of the cache's {heads}")
     return R, Hq, max_pages
 
 
@@ -577,27 +577,23 @@ def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, 
     lens and free_state themselves), the first new token of each request, the slot
     of each new token (`capacity` of them, -1 behind the last) and 0 or PLAN_* bits
     (then nothing changed)."""
+    if lens_out is None and free_state_out is None and workspace is None and stream is None:
+        r = _calls.cache_plan(lens, delta, block_table, free_ring, free_state, page_size, capacity)
+        if r is not None:
+            if r[0]:
+                raise CpattnError(r[0], "cpattn_cache_plan")
+            return r[1:]
     if stream is not None:  # outputs and workspaces are allocated for the stream the call runs on
         with torch.cuda.stream(stream):
             return cache_plan(lens, delta, block_table, free_ring, free_state, page_size, capacity, lens_out,
                               free_state_out, workspace)
-    try:
-        (R, max_pages), (num_pages,), dev = block_table.shape, free_ring.shape, block_table.get_device()
-        right = (lens.shape == (R,) and delta.shape == (R,) and free_state.shape == (2,)
-                 and block_table.dtype is lens.dtype is delta.dtype is free_ring.dtype is free_state.dtype is torch.int32
-                 and lens.get_device() == dev and delta.get_device() == dev and free_ring.get_device() == dev
-                 and free_state.get_device() == dev and block_table.is_contiguous() and lens.is_contiguous()
-                 and delta.is_contiguous() and free_ring.is_contiguous() and free_state.is_contiguous())
-    except (AttributeError, TypeError, ValueError):
-        right = False
-    if not right:
-        R, max_pages = _batch(block_table, lens)
-        _expect(delta, "delta", (R,), torch.int32, block_table)
-        if not isinstance(free_ring, torch.Tensor) or free_ring.dim() != 1:
-            raise ValueError("free_ring must be a [num_pages] tensor")
-        _expect(free_ring, "free_ring", free_ring.shape, torch.int32, block_table)
-        _expect(free_state, "free_state", (2,), torch.int32, block_table)
-        num_pages, dev = free_ring.shape[0], block_table.get_device()
+    R, max_pages = _batch(block_table, lens)
+    _expect(delta, "delta", (R,), torch.int32, block_table)
+    if not isinstance(free_ring, torch.Tensor) or free_ring.dim() != 1:
+        raise ValueError("free_ring must be a [num_pages] tensor")
+    _expect(free_ring, "free_ring", free_ring.shape, torch.int32, block_table)
+    _expect(free_state, "free_state", (2,), torch.int32, block_table)
+    num_pages, dev = free_ring.shape[0], block_table.get_device()
     if lens_out is not None:
         _expect(lens_out, "lens_out", (R,), torch.int32, block_table)
     if free_state_out is not None:
@@ -638,25 +634,21 @@ def cache_append_(k_new, v_new, slots, k_cache, v_cache, k_bounds=None, kv_amax=
     """New rows into a paged cache (in place): k_new, v_new [N, kv_heads, D] with
     contiguous columns (views of [kv_heads, N, D] too), slots [N] int64 (negative:
     skipped).  k_bounds [num_pages, kv_heads, 2, D] is kept up to date when given."""
+    if stream is None:
+        r = _calls.cache_append(k_new, v_new, slots, k_cache, v_cache, k_bounds, kv_amax)
+        if r is not None:
+            if r[0]:
+                raise CpattnError(r[0], "cpattn_cache_append")
+            return k_cache, v_cache
     (num_pages, heads, page_size, D), dtype, code, dev = _cache(k_cache, v_cache, kv_amax)
-    try:
-        (N,), ks, vs = slots.shape, k_new.stride(), v_new.stride()
-        right = (k_new.shape == (N, heads, D) and v_new.shape == (N, heads, D) and k_new.dtype is v_new.dtype is dtype
-                 and ks[2] == 1 == vs[2] and slots.dtype is torch.int64 and slots.is_contiguous()
-                 and k_new.get_device() == dev and v_new.get_device() == dev and slots.get_device() == dev
-                 and (k_bounds is None or (k_bounds.shape == (num_pages, heads, 2, D) and k_bounds.dtype is k_cache.dtype
-                                           and k_bounds.get_device() == dev and k_bounds.is_contiguous())))
-    except (AttributeError, TypeError, ValueError):
-        right = False
-    if not right:
-        if k_bounds is not None:
-            _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_cache.dtype, k_cache)
-        if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-            raise ValueError("slots must be a [N] tensor")
-        N = slots.shape[0]
-        _expect(slots, "slots", (N,), torch.int64, k_cache)
-        ks = _rows(k_new, "k_new", (N, heads, D), dtype, k_cache)
-        vs = _rows(v_new, "v_new", (N, heads, D), dtype, k_cache)
+    if k_bounds is not None:
+        _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_cache.dtype, k_cache)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a [N] tensor")
+    N = slots.shape[0]
+    _expect(slots, "slots", (N,), torch.int64, k_cache)
+    ks = _rows(k_new, "k_new", (N, heads, D), dtype, k_cache)
+    vs = _rows(v_new, "v_new", (N, heads, D), dtype, k_cache)
     s = _here(k_cache, "k_cache", dev)
     if stream is not None:
         s = stream.cuda_stream
@@ -670,7 +662,13 @@ def select_pages(q, k_bounds, block_table, lens, page_size: int, budget: int, ke
     """The pages one new token per request attends to: int32 [R, kv_heads, budget],
     ascending, -1 behind the last (see cpattn_select_pages in include/cpattn.h).
     q [R, Hq, D]; k_bounds [num_pages, kv_heads, 2, D] as cache_append_ keeps it."""
-    if stream is not None:
+    if stream is None:
+        r = _calls.select_pages(q, k_bounds, block_table, lens, page_size, budget, keep_first)
+        if r is not None:
+            if r[0]:
+                raise CpattnError(r[0], "cpattn_select_pages")
+            return r[1]
+    else:
         with torch.cuda.stream(stream):
             return select_pages(q, k_bounds, block_table, lens, page_size, budget, keep_first)
     if not isinstance(k_bounds, torch.Tensor) or k_bounds.dim() != 4:
@@ -680,9 +678,8 @@ def select_pages(q, k_bounds, block_table, lens, page_size: int, budget: int, ke
     dev = k_bounds.get_device()
     if 0 in k_bounds.shape:
         raise ValueError(f"k_bounds is empty: {tuple(k_bounds.shape)}")
-    if not _fits(k_bounds, (num_pages, heads, 2, D), k_bounds.dtype, dev):
-        _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_bounds.dtype)
-    R, Hq, max_pages = _queries(q, block_table, lens, dtype, heads, D, k_bounds, dev)
+    _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_bounds.dtype)
+    R, Hq, max_pages = _queries(q, block_table, lens, dtype, heads, D, k_bounds)
     if budget < 1 or keep_first < 0 or budget <= keep_first:
         raise ValueError(f"budget ({budget}) must be above keep_first ({keep_first}), and keep_first not negative")
     s = _here(q, "q", dev)
@@ -697,26 +694,28 @@ def decode_workspace_bytes(R, Hq, Hkv, D) -> int:
     return int(lib.cpattn_decode_workspace_bytes(R, Hq, Hkv, D))
 
 
-_decode_need = {}  # (device, Hq, Hkv, D) -> workspace bytes
-
-
 def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, scale=None, out_dtype=None, out=None,
            lse=None, workspace=None, stream=None):
     """Attention of one new token per request over a paged cache: (o [R, Hq, D] like
     q, or of out_dtype; lse fp32 [R, Hq]).  pages: int32 [R, kv_heads, budget] as
     select_pages gives them, or None for every page."""
+    if out_dtype is None and out is None and lse is None and workspace is None and stream is None:
+        r = _calls.decode(q, k_cache, v_cache, block_table, lens, pages, kv_amax, scale)
+        if r is not None:
+            if r[0]:
+                raise CpattnError(r[0], "cpattn_decode")
+            return r[1:]
     if stream is not None:
         with torch.cuda.stream(stream):
             return decode(q, k_cache, v_cache, block_table, lens, pages, kv_amax, scale, out_dtype, out, lse, workspace)
     (num_pages, heads, page_size, D), dtype, code, dev = _cache(k_cache, v_cache, kv_amax)
-    R, Hq, max_pages = _queries(q, block_table, lens, dtype, heads, D, k_cache, dev)
+    R, Hq, max_pages = _queries(q, block_table, lens, dtype, heads, D, k_cache)
     budget = 0
     if pages is not None:
         if not isinstance(pages, torch.Tensor) or pages.dim() != 3:
             raise ValueError("pages must be a [R, kv_heads, budget] tensor")
         budget = pages.shape[2]
-        if not _fits(pages, (R, heads, budget), torch.int32, dev):
-            _expect(pages, "pages", (R, heads, budget), torch.int32, k_cache)
+        _expect(pages, "pages", (R, heads, budget), torch.int32, k_cache)
     out_dtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
     if out_dtype != torch.bfloat16 and out_dtype != torch.float32:
         raise TypeError(f"unsupported dtype {out_dtype}")
@@ -725,23 +724,14 @@ def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, sca
     if lse is not None:
         _expect(lse, "lse", (R, Hq), torch.float32, k_cache)
     s = _here(q, "q", dev)
-    need = _decode_need.get((dev, Hq, heads, D))
-    if need is None:
-        need = _decode_need[dev, Hq, heads, D] = decode_workspace_bytes(R, Hq, heads, D)
-    if out is not None:
-        o = out
-    else:
-        o = torch.empty_like(q) if out_dtype is dtype else torch.empty_like(q, dtype=out_dtype)
-    lse = torch.empty(R, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
-    if workspace is None:
-        workspace, ws_bytes = torch.empty(need, dtype=torch.uint8, device=q.device), need
-    else:
-        workspace = _scratch(workspace, need, q)
-        ws_bytes = workspace.numel() * workspace.element_size()
+    need = decode_workspace_bytes(R, Hq, heads, D)
+    o = torch.empty_like(q, dtype=out_dtype) if out is None else out
+    lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else _scratch(workspace, need, q)
     _check(lib.cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                              lens.data_ptr(), _p(pages), o.data_ptr(), lse.data_ptr(), R, Hq, heads, D, page_size,
                              max_pages, num_pages, budget, D ** -0.5 if scale is None else scale, _p(kv_amax),
-                             workspace.data_ptr(), ws_bytes, FP32 if dtype == torch.float32 else BF16, code,
+                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), FP32 if dtype == torch.float32 else BF16, code,
                              FP32 if out_dtype == torch.float32 else BF16, s), "cpattn_decode")
     return o, lse
 
