@@ -4,22 +4,29 @@
 // page's bounds could have, over the query heads of the group:
 //     score = max_i sum_d max(q_id lo_d, q_id hi_d)
 //           = max_i sum_d (min(q_id, 0) lo_d + max(q_id, 0) hi_d)
-// summed in 64 bits and rounded once to fp32: products of 16-bit values are
-// exact there and their sums almost always, so that the order of summation
-// does not decide between near pages.  The `budget` pages with the largest
-// scores are listed in ascending order, ties to the lower page; the newest
-// page and the first keep_first pages are always among them.
+// in 64 bits, rounded once to fp32: products of 16-bit values are exact there and
+// their sums almost always, so that the order of summation does not decide
+// between near pages.  The `budget` pages with the largest scores are listed in
+// ascending order, ties to the lower page; the newest page and the first
+// keep_first pages are always among them.
+//
+// Scoring every page in 64 bits is what that would cost most (64 products a cycle
+// and SM).  For 16- and 8-bit bounds the tensor cores score in fp32 first, with an
+// error below eps = 2D 2^-23 sum |q| max |bound| (2D additions of at most two units
+// in the last place each): of a page more than 2 eps above or below the budget-th
+// largest score it is then known on which side it stands, and only those between,
+// a few, are scored in 64 bits.
 //
 // One cluster of thread blocks takes one (request, kv head): every block scores
 // a stretch of pages and sends the scores to the first block's shared memory,
 // which finds the threshold by a radix search of eight bits at a time and lists
 // the pages.  A page's bounds are read once; what bounds the kernel is the
 // chain of latencies from the lengths over the page table and the bounds to the
-// search, so the loads of a warp's next pages are under way while it sums, and
-// the pages are spread over as many blocks as the device holds at once.
+// search, so the pages are spread over as many blocks as the device holds at once.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cpattn.h"
 #include "kernels.h"
@@ -52,14 +59,23 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// the number that order_key maps to k
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
 // W consecutive words, in place.
 template <int W>
 __device__ __forceinline__ void load_packed(const void* p, uint32_t (&w)[W]) {
+  if constexpr (W < 4) {
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
 #pragma unroll
-  for (int i = 0; i < W; i += 4)
-    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                 : "l"(static_cast<const char*>(p) + 4 * i));
+    for (int i = 0; i < W; i += 4)
+      asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "l"(static_cast<const char*>(p) + 4 * i));
+  }
 }
 
 // c (8 pages x 8 heads, 64 bits) += a (8 pages x 4 columns) b (4 columns x 8 heads)
@@ -68,74 +84,71 @@ __device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
                : "+d"(c[0]), "+d"(c[1])
                : "d"(a), "d"(b));
 }
+// c (16 pages x 8 heads, fp32) += a (16 pages x 16 columns) b (16 columns x 8 heads)
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct Pair {  // what a cluster works on
+  int r, h, first, n;  // request, kv head; this block's stretch of pages
+  const int32_t* table;
+};
 
 template <typename CT, int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
+__device__ __forceinline__ const CT* bounds_of(const SelectArgs& a, const Pair& p, int page) {
+  return static_cast<const CT*>(a.bounds) + ((size_t)page * a.Hkv + p.h) * 2 * D;
+}
+__device__ __forceinline__ bool in_pool(const SelectArgs& a, int page) { return (unsigned)page < (unsigned)a.num_pages; }
+
+// Scores of the block's pages in 64 bits on the tensor cores, 8 pages a warp.
+template <typename CT, int D>
+struct Exact {
   // A warp takes 8 pages at a time, 4 lanes each, in steps of W words (E columns) of
   // a lane's low and high bounds.
-  constexpr int P = Unpack<CT>::kPerWord;
-  constexpr int W = D / (4 * P) < 8 ? D / (4 * P) : 8, E = W * P, STEPS = D / (4 * E);
-  extern __shared__ uint32_t s_key[];      // the first block's: the keys of all pages
-  __shared__ double2 s_q[STEPS * E][32];   // (min(q, 0), max(q, 0)) of 4 columns x 8 heads
-  __shared__ uint32_t s_hist[256], s_bin[kThreads];
-  __shared__ uint32_t s_pick[3], s_found, s_warp[kWarps], s_warp2[kWarps];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int pair = blockIdx.x / ranks, r = pair / a.Hkv, h = pair % a.Hkv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int32_t* out = a.sel + (size_t)pair * a.budget;
+  static constexpr int P = Unpack<CT>::kPerWord;
+  static constexpr int W = D / (4 * P) < 8 ? D / (4 * P) : 8, E = W * P, STEPS = D / (4 * E);
+  static constexpr int kQueryBytes = STEPS * E * 32 * 16;
 
-  after_previous();
-  const long long cap = (long long)a.max_pages << a.shift;
-  long long len = a.lens[r];
-  if (len < 0 || len > cap) {
-    if (tid == 0) atomicOr(a.err, kErrPage);
-    len = len < 0 ? 0 : cap;
-  }
-  const int held = (int)((len + (1 << a.shift) - 1) >> a.shift);
-  if (held <= a.budget) {  // everything is selected (the whole cluster leaves here)
-    for (int j = rank * kThreads + tid; j < a.budget; j += ranks * kThreads) out[j] = j < held ? j : -1;
-    return;
-  }
+  uint32_t lo[W], hi[W];
+  int page, page_next;
 
-  cluster.barrier_arrive();  // no block writes to the first one before that has started
-
-  const int per = (held + ranks - 1) / ranks;
-  const int first = min(rank * per, held), n = min(per, held - first);
-  const int g = lane >> 2, t = lane & 3;
-  uint32_t* keys = cluster.map_shared_rank(s_key, 0);
-  const int32_t* table = a.table + (size_t)r * a.max_pages + first;
-  auto page_of = [&](int i) { return table[min(i, n - 1)]; };  // only for n > 0
-  auto load = [&](int page, int step, uint32_t (&lo)[W], uint32_t (&hi)[W]) {
-    const int p = page >= 0 && page < a.num_pages ? page : 0;
-    const CT* b = static_cast<const CT*>(a.bounds) + ((size_t)p * a.Hkv + h) * 2 * D + step * 4 * E + t * E;
+  __device__ __forceinline__ int page_of(const Pair& p, int i) const { return p.table[p.first + min(i, p.n - 1)]; }
+  __device__ __forceinline__ void load(const SelectArgs& a, const Pair& p, int step) {
+    const CT* b = bounds_of<CT, D>(a, p, in_pool(a, page) ? page : 0) + step * 4 * E + (threadIdx.x & 3) * E;
     load_packed(b, lo);
     load_packed(b + D, hi);
-  };
-  for (int h0 = 0; h0 < a.group; h0 += 8) {
-    uint32_t lo[W], hi[W];
-    int i0 = warp * 8, page = 0, page_next = 0;
-    if (i0 < n) {
-      page = page_of(i0 + g);
-      page_next = page_of(i0 + kWarps * 8 + g);
-      load(page, 0, lo, hi);
-    }
-    __syncthreads();
-    for (int i = tid; i < 8 * D; i += kThreads) {
+  }
+  __device__ __forceinline__ void queries(const SelectArgs&, int, int, int) {}
+  // the first pages' loads
+  __device__ __forceinline__ void begin(const SelectArgs& a, const Pair& p) {
+    const int g = (threadIdx.x & 31) >> 2, i0 = (threadIdx.x >> 5) * 8;
+    if (i0 >= p.n) return;
+    page = page_of(p, i0 + g);
+    page_next = page_of(p, i0 + kWarps * 8 + g);
+    load(a, p, 0);
+  }
+
+  __device__ __forceinline__ void stage(const SelectArgs& a, const Pair& p, int h0, char* s, float*) {
+    double2(*s_q)[32] = reinterpret_cast<double2(*)[32]>(s);  // (min(q, 0), max(q, 0)) of 4 columns x 8 heads
+    for (int i = threadIdx.x; i < 8 * D; i += kThreads) {
       const int head = i / D, d = i % D;
       float x = 0.f;
-      if (h0 + head < a.group) {
-        const size_t at = ((size_t)r * a.Hq + (size_t)h * a.group + h0 + head) * D + d;
-        x = a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at])
-                     : static_cast<const float*>(a.q)[at];
-      }
+      if (h0 + head < a.group)
+        x = static_cast<const float*>(a.q)[((size_t)p.r * a.Hq + (size_t)p.h * a.group + h0 + head) * D + d];
       s_q[d / (4 * E) * E + d % E][head * 4 + d / E % 4] = make_double2(fminf(x, 0.f), fmaxf(x, 0.f));
     }
-    if (h0 == 0) cluster.barrier_wait();
-    __syncthreads();
-    for (; i0 < n; i0 += kWarps * 8) {
-      const int i = i0 + g, j = first + i;
-      const bool there = page >= 0 && page < a.num_pages;
+  }
+
+  template <typename Put>
+  __device__ __forceinline__ float score(const SelectArgs& a, const Pair& p, int h0, const char* s, Put put) {
+    const double2(*s_q)[32] = reinterpret_cast<const double2(*)[32]>(s);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    for (int i0 = warp * 8; i0 < p.n; i0 += kWarps * 8) {
+      const bool there = in_pool(a, page);
       if (!there && t == 0) atomicOr(a.err, kErrPage);
       double acc[4][2] = {};
 #pragma unroll
@@ -147,12 +160,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
           Unpack<CT>::word(hi[w], fhi + w * P);
         }
         if (step + 1 < STEPS) {
-          load(page, step + 1, lo, hi);
+          load(a, p, step + 1);
         } else {
           page = page_next;
-          if (i0 + kWarps * 8 < n) {
-            load(page, 0, lo, hi);
-            page_next = page_of(i0 + 2 * kWarps * 8 + g);
+          if (i0 + kWarps * 8 < p.n) {
+            load(a, p, 0);
+            page_next = page_of(p, i0 + 2 * kWarps * 8 + g);
           }
         }
 #pragma unroll
@@ -171,119 +184,457 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       }
       key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
       key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
-      if (t == 0 && i < n) {
-        if (j < a.keep_first || j == held - 1) key = 0xffffffffu;
-        keys[j] = h0 == 0 ? key : max(key, keys[j]);
-      }
+      if (t == 0 && i0 + g < p.n) put(p.first + i0 + g, key);
+    }
+    return 0.f;
+  }
+};
+
+// The same in fp32 with bf16 operands, 16 pages a warp; also the largest |bound|
+// and, staging, the largest sum |q| of a head.
+template <typename CT, int D>
+struct Approx {
+  static constexpr int W = D * (int)sizeof(CT) / 16;  // words of a lane's quarter of a row
+  static constexpr int kQueryBytes = D / 32 * 2 * 32 * 16;
+
+  // A lane's quarter of a row are its 16-byte pieces t, t + 4, ...: entry e of 8 columns is
+  // piece e (bf16) or half of piece e / 2 (e4m3).
+  __device__ static __forceinline__ void load(const CT* row, int t, uint32_t (&w)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "l"(reinterpret_cast<const char*>(row) + 16 * (i + t)));
+  }
+
+  uint32_t q[4], lo[2][W], hi[2][W];
+  int page[2];
+
+  // a warp's head and a lane's 8 columns of it
+  __device__ __forceinline__ void queries(const SelectArgs& a, int r, int h, int h0) {
+    static_assert(kWarps == 8, "a warp for each head");
+    const int lane = threadIdx.x & 31, head = threadIdx.x >> 5;
+    q[0] = q[1] = q[2] = q[3] = 0u;
+    if (h0 + head < a.group && lane < D / 8)
+      load_packed(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)r * a.Hq + (size_t)h * a.group + h0 + head) * D + lane * 8, q);
+  }
+  __device__ __forceinline__ void pages(const SelectArgs& a, const Pair& p, int i0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) page[r] = p.table[p.first + min(i0 + g + 8 * r, p.n - 1)];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const CT* b = bounds_of<CT, D>(a, p, in_pool(a, page[r]) ? page[r] : 0);
+      load(b, t, lo[r]);
+      load(b + D, t, hi[r]);
     }
   }
-  cluster.sync();
-  if (rank != 0) return;
-
-  // The pages that are always listed need no search: their key is the largest.
-  // The others: first the leading bits that all keys share, then eight bits at a
-  // time until the bin of the threshold is small enough to rank its keys directly.
-  const int always = min(a.keep_first, held - 1) + 1;
-  const uint32_t kAlways = 0xffffffffu;
-  uint32_t any = 0u, all = 0xffffffffu;
-  for (int i = tid; i < held; i += kThreads) {
-    const uint32_t key = s_key[i];
-    if (key != kAlways) any |= key, all &= key;
+  // the first pages' loads
+  __device__ __forceinline__ void begin(const SelectArgs& a, const Pair& p) {
+    const int i0 = (threadIdx.x >> 5) * 16;
+    if (i0 < p.n) pages(a, p, i0);
   }
-  s_hist[tid] = 0;
+
+  // s: [entry][min(q, 0), max(q, 0)][lane] 16 bytes
+  __device__ __forceinline__ void stage(const SelectArgs&, const Pair&, int h0, char* s, float* norm) {
+    const int lane = threadIdx.x & 31, head = threadIdx.x >> 5;
+    // the lane and entry that columns 8 * lane .. + 7 belong to: see load()
+    const int t = sizeof(CT) == 2 ? lane & 3 : (lane >> 1) & 3;
+    const int e = sizeof(CT) == 2 ? lane >> 2 : (lane >> 3) * 2 + (lane & 1);
+    float sum = 0.f;
+    uint32_t neg[4], pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[2];
+      Unpack<__nv_bfloat16>::word(q[i], f);
+      sum += fabsf(f[0]) + fabsf(f[1]);
+      const uint32_t minus = ((q[i] & 0x8000u) ? 0xffffu : 0u) | ((q[i] & 0x80000000u) ? 0xffff0000u : 0u);
+      neg[i] = q[i] & minus;
+      pos[i] = q[i] & ~minus;
+    }
+    if (lane < D / 8) {
+      uint4* to = reinterpret_cast<uint4*>(s) + e * 64 + head * 4 + t;
+      to[0] = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+      to[32] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) norm[head] = h0 == 0 ? sum : fmaxf(norm[head], sum);
+  }
+
+  // words 2i, 2i + 1 (e4m3: word i) of a lane's quarter as two bf16 pairs
+  __device__ static __forceinline__ void pairs(const uint32_t (&w)[W], int i, uint32_t& x, uint32_t& y) {
+    if constexpr (sizeof(CT) == 2) {
+      x = w[2 * i], y = w[2 * i + 1];
+    } else {
+      float f[4];
+      Unpack<E4m3>::word(w[i], f);
+      const __nv_bfloat162 u = __floats2bfloat162_rn(f[0], f[1]), v = __floats2bfloat162_rn(f[2], f[3]);
+      x = *reinterpret_cast<const uint32_t*>(&u), y = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+  __device__ static __forceinline__ __nv_bfloat162 as2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+
+  template <typename Put>
+  __device__ __forceinline__ float score(const SelectArgs& a, const Pair& p, int h0, const char* s, Put put) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    __nv_bfloat162 most = __float2bfloat162_rn(0.f);
+    for (int i0 = warp * 16; i0 < p.n; i0 += kWarps * 16) {
+      if (i0 > warp * 16) pages(a, p, i0);
+      float c[4][4] = {};
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        const uint4 qn = reinterpret_cast<const uint4*>(s)[e * 64 + lane], qp = reinterpret_cast<const uint4*>(s)[e * 64 + 32 + lane];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x[2], y[2], z[2], w[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            pairs(lo[r], 2 * e + half, x[r], y[r]);
+            pairs(hi[r], 2 * e + half, z[r], w[r]);
+            most = __hmax2(most, __hmax2(__hmax2(__habs2(as2(x[r])), __habs2(as2(y[r]))), __hmax2(__habs2(as2(z[r])), __habs2(as2(w[r])))));
+          }
+          mma_bf16(c[2 * half], x[0], x[1], y[0], y[1], half ? qn.z : qn.x, half ? qn.w : qn.y);
+          mma_bf16(c[2 * half + 1], z[0], z[1], w[0], w[1], half ? qp.z : qp.x, half ? qp.w : qp.y);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool there = in_pool(a, page[r]);
+        if (!there && t == 0) atomicOr(a.err, kErrPage);
+        uint32_t key = 0u;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int i = 2 * r + m;
+          if (there && h0 + 2 * t + m < a.group) key = max(key, order_key((c[0][i] + c[1][i]) + (c[2][i] + c[3][i])));
+        }
+        key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+        key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
+        if (t == 0 && i0 + g + 8 * r < p.n) put(p.first + i0 + g + 8 * r, key);
+      }
+    }
+    return fmaxf(__low2float(most), __high2float(most));
+  }
+
+  // The score of one page in 64 bits, by a whole warp.
+  __device__ static uint32_t rescore(const SelectArgs& a, const Pair& p, int j) {
+    const int lane = threadIdx.x & 31;
+    constexpr int V = D / 32;  // columns of a lane
+    const int page = p.table[j];
+    if (!in_pool(a, page)) return 0u;
+    const CT* b = bounds_of<CT, D>(a, p, page) + lane * V;
+    float lo[V], hi[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if constexpr (sizeof(CT) == 2) {
+        lo[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(b)[e]);
+        hi[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(b + D)[e]);
+      } else {
+        float f[4];
+        Unpack<E4m3>::word(reinterpret_cast<const uint8_t*>(b)[e], f);
+        lo[e] = f[0];
+        Unpack<E4m3>::word(reinterpret_cast<const uint8_t*>(b + D)[e], f);
+        hi[e] = f[0];
+      }
+    }
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)p.r * a.Hq + (size_t)p.h * a.group) * D + lane * V;
+    uint32_t key = 0u;
+    for (int m = 0; m < a.group; ++m) {
+      double sum = 0.;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = __bfloat162float(q[(size_t)m * D + e]);
+        sum = fma((double)fminf(x, 0.f), (double)lo[e], sum);
+        sum = fma((double)fmaxf(x, 0.f), (double)hi[e], sum);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      key = max(key, order_key((float)sum));
+    }
+    return key;
+  }
+};
+
+constexpr uint32_t kAlways = 0xffffffffu;  // key of a page that is listed whatever its score
+
+struct Search {
+  uint32_t hist[256], bin[kThreads], warp[3][kWarps], pick[3], found;
+};
+
+// The budget-th largest of n keys: every key above `threshold` is taken, and the
+// first `need` equal to it.  First the leading bits that all keys share, then
+// eight bits at a time until the bin of the threshold is small enough to rank its
+// keys directly.  `itself`: the threshold has to be that key itself, not a
+// number below a bin that is taken whole.
+__device__ __noinline__ void find_threshold(const uint32_t* keys, int n, int budget, bool itself, Search& s, uint32_t& threshold, int& need) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto each = [&](auto f) {
+    for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+      const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+      f(k.x);
+      if (i + 1 < n) f(k.y);
+      if (i + 2 < n) f(k.z);
+      if (i + 3 < n) f(k.w);
+    }
+  };
+  uint32_t any = 0u, all = 0xffffffffu, always = 0u;
+  each([&](uint32_t key) {
+    if (key == kAlways) ++always;
+    else any |= key, all &= key;
+  });
   any = __reduce_or_sync(0xffffffffu, any);
   all = __reduce_and_sync(0xffffffffu, all);
-  if (lane == 0) s_warp[warp] = any, s_warp2[warp] = all;
-  if (tid == 0) s_found = 0;
+  always = __reduce_add_sync(0xffffffffu, always);
   __syncthreads();
-  for (int w = 0; w < kWarps; ++w) any |= s_warp[w], all &= s_warp2[w];
+  s.hist[tid & 255] = 0;
+  if (lane == 0) s.warp[0][warp] = any, s.warp[1][warp] = all, s.warp[2][warp] = always;
+  if (tid == 0) s.found = 0;
+  __syncthreads();
+  always = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) any |= s.warp[0][w], all &= s.warp[1][w], always += s.warp[2][w];
   int low = 32 - __clz(any ^ all);               // bits below `low` differ
   uint32_t prefix = low < 32 ? any >> low : 0u;  // of the threshold
-  int need = a.budget - always;                  // keys wanted among those that share the prefix
-  uint32_t threshold = any;                      // every key above it, and `need` equal to it
-  if (need == 0) low = 0, threshold = kAlways - 1u;
+  need = budget - (int)always;                   // keys wanted among those that share the prefix
+  threshold = any;
+  if (need <= 0) low = 0, need = 0, threshold = kAlways - 1u;
   while (low > 0) {
     const int above = low;
     low = max(0, low - 8);
     const uint32_t digits = (1u << (above - low)) - 1u;
-    for (int i = tid; i < held; i += kThreads) {
-      const uint32_t key = s_key[i];
-      if (key != kAlways && (above == 32 || (key >> above) == prefix)) atomicAdd(&s_hist[(key >> low) & digits], 1u);
-    }
+    each([&](uint32_t key) {
+      if (key != kAlways && (above == 32 || (key >> above) == prefix)) atomicAdd(&s.hist[(key >> low) & digits], 1u);
+    });
     __syncthreads();
     // thread b: keys in bin 255 - b; inclusive sums from the top
-    const uint32_t c = s_hist[255 - tid];
+    const uint32_t c = s.hist[255 - tid];
     uint32_t up = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += x;
     }
-    if (lane == 31) s_warp[warp] = up;
+    if (lane == 31) s.warp[0][warp] = up;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      if (w < warp) up += s_warp[w];
-    if (up >= (uint32_t)need && up - c < (uint32_t)need) s_pick[0] = 255 - tid, s_pick[1] = need - (up - c), s_pick[2] = c;
-    s_hist[255 - tid] = 0;
+      if (w < warp) up += s.warp[0][w];
+    if (up >= (uint32_t)need && up - c < (uint32_t)need) s.pick[0] = 255 - tid, s.pick[1] = need - (up - c), s.pick[2] = c;
+    s.hist[255 - tid] = 0;
     __syncthreads();
-    prefix = (above == 32 ? 0u : prefix << (above - low)) | s_pick[0];
-    need = (int)s_pick[1];
+    prefix = (above == 32 ? 0u : prefix << (above - low)) | s.pick[0];
+    need = (int)s.pick[1];
     threshold = prefix << low;
-    const uint32_t in_bin = s_pick[2];
+    const uint32_t in_bin = s.pick[2];
     if (low == 0) break;
-    if (in_bin == (uint32_t)need) {  // the whole bin is taken; a key below it exists, so threshold > 0
+    if (in_bin == (uint32_t)need && !itself && threshold > 0u) {  // the whole bin is taken
       threshold -= 1u;
       need = 0;
       break;
     }
     if (in_bin <= (uint32_t)kThreads) {  // rank the bin's keys: one for each thread
-      for (int i = tid; i < held; i += kThreads) {
-        const uint32_t key = s_key[i];
-        if (key != kAlways && (key >> low) == prefix) s_bin[atomicAdd(&s_found, 1u)] = key;
-      }
+      each([&](uint32_t key) {
+        if (key != kAlways && (key >> low) == prefix) s.bin[atomicAdd(&s.found, 1u)] = key;
+      });
       __syncthreads();
       if (tid < (int)in_bin) {
-        const uint32_t key = s_bin[tid];
+        const uint32_t key = s.bin[tid];
         uint32_t more = 0, same = 0;
-        for (uint32_t i = 0; i < in_bin; ++i) more += s_bin[i] > key, same += s_bin[i] == key;
+        for (uint32_t i = 0; i < in_bin; ++i) more += s.bin[i] > key, same += s.bin[i] == key;
         // equal keys write the same two numbers
-        if (more < (uint32_t)need && more + same >= (uint32_t)need) s_pick[0] = key, s_pick[1] = need - more;
+        if (more < (uint32_t)need && more + same >= (uint32_t)need) s.pick[0] = key, s.pick[1] = need - more;
       }
       __syncthreads();
-      threshold = s_pick[0];
-      need = (int)s_pick[1];
+      threshold = s.pick[0];
+      need = (int)s.pick[1];
       break;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename CT, int D>
+__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
+  constexpr bool kApprox = sizeof(CT) < 4;
+  using Scores = std::conditional_t<kApprox, Approx<CT, D>, Exact<CT, D>>;
+  extern __shared__ __align__(16) uint32_t s_key[];  // the first block's: the keys of all pages
+  __shared__ __align__(16) char s_q[Scores::kQueryBytes];
+  __shared__ Search s_search;
+  __shared__ uint32_t s_count[2][kWarps], s_list[kThreads], s_listed;
+  __shared__ float s_most[kMaxCluster], s_warp_most[kWarps];
+  __shared__ float s_norm[8];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int pair = blockIdx.x / ranks;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t* out = a.sel + (size_t)pair * a.budget;
+  Scores scores;
+  Pair p = {pair / a.Hkv, pair % a.Hkv, 0, 0, nullptr};
+
+  after_previous();
+  scores.queries(a, p.r, p.h, 0);
+  const long long cap = (long long)a.max_pages << a.shift;
+  long long len = a.lens[p.r];
+  if (len < 0 || len > cap) {
+    if (tid == 0) atomicOr(a.err, kErrPage);
+    len = len < 0 ? 0 : cap;
+  }
+  const int held = (int)((len + (1 << a.shift) - 1) >> a.shift);
+  if (held <= a.budget) {  // everything is selected (the whole cluster leaves here)
+    for (int j = rank * kThreads + tid; j < a.budget; j += ranks * kThreads) out[j] = j < held ? j : -1;
+    return;
+  }
+  if (tid == 0) s_listed = 0u;
+  cluster.barrier_arrive();  // no block writes to the first one before that has started
+
+  const int per = (held + ranks - 1) / ranks;
+  p.first = min(rank * per, held);
+  p.n = min(per, held - p.first);
+  p.table = a.table + (size_t)p.r * a.max_pages;
+  uint32_t* keys = cluster.map_shared_rank(s_key, 0);
+  for (int h0 = 0; h0 < a.group; h0 += 8) {
+    if (h0 > 0) {
+      scores.queries(a, p.r, p.h, h0);
+      __syncthreads();
+    }
+    scores.begin(a, p);
+    scores.stage(a, p, h0, s_q, s_norm);
+    if (h0 == 0) cluster.barrier_wait();
+    __syncthreads();
+    float most = scores.score(a, p, h0, s_q, [&](int j, uint32_t key) {
+      if (j < a.keep_first || j == held - 1) key = kAlways;
+      keys[j] = h0 == 0 ? key : max(key, keys[j]);
+    });
+    if constexpr (kApprox) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      if (lane == 0 && h0 == 0) s_warp_most[warp] = most;
+    }
+  }
+  if constexpr (kApprox) {
+    __syncthreads();
+    if (tid == 0) {
+      float most = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) most = fmaxf(most, s_warp_most[w]);
+      *cluster.map_shared_rank(&s_most[rank], 0) = most;
+    }
+  }
+  cluster.sync();
+  if (rank != 0) return;
+
+  uint32_t threshold;
+  int need;
+  find_threshold(s_key, held, a.budget, kApprox, s_search, threshold, need);
+  // a stretch of pages for each warp, in steps of 32
+  const int stretch = ((held + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = min(warp * stretch, held), w1 = min(w0 + stretch, held);
+  if constexpr (kApprox) {
+    if (threshold != kAlways - 1u) {
+      // [low, high]: the keys within 2 eps of the threshold
+      float norm = 0.f, most = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) norm = fmaxf(norm, s_norm[i]);
+      for (int i = 0; i < ranks; ++i) most = fmaxf(most, s_most[i]);
+      const float at = key_value(threshold);
+      const float eps = norm * most * ((D / 2 + 2) * 0x1p-23f) * 1.01f + fabsf(at) * 0x1p-22f;
+      uint32_t low = 0u, high = kAlways - 1u;
+      if (threshold != 0u && eps < 1e37f && fabsf(at) < 1e37f)
+        low = order_key(__fadd_rd(at, -2.f * eps)), high = min(high, order_key(__fadd_ru(at, 2.f * eps)));
+      uint32_t above = 0, within = 0;
+      for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t key = s_key[i];
+        above += key > high;
+        within += key >= low && key <= high;
+      }
+      above = __reduce_add_sync(0xffffffffu, above);
+      within = __reduce_add_sync(0xffffffffu, within);
+      if (lane == 0) s_count[0][warp] = above, s_count[1][warp] = within;
+      __syncthreads();
+      above = within = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) above += s_count[0][w], within += s_count[1][w];
+      if (above + within == (uint32_t)a.budget) {  // those within are taken too
+        threshold = low - 1u;
+        need = 0;
+        __syncthreads();
+      } else if (within <= (uint32_t)kThreads) {
+        // list them, score a page with each warp, rank a page with each thread
+        for (int i = w0 + lane; i < w1; i += 32) {
+          const uint32_t key = s_key[i];
+          if (key >= low && key <= high) s_list[atomicAdd(&s_listed, 1u)] = i;
+          else s_key[i] = key > high ? kAlways : 0u;
+        }
+        __syncthreads();
+        for (uint32_t i = warp; i < within; i += kWarps) {
+          const uint32_t exact = Scores::rescore(a, p, (int)s_list[i]);
+          if (lane == 0) s_search.bin[i] = exact;
+        }
+        __syncthreads();
+        if (tid < (int)within) {
+          const uint32_t key = s_search.bin[tid], page = s_list[tid];
+          uint32_t before = above;
+          for (uint32_t i = 0; i < within; ++i)
+            before += s_search.bin[i] > key || (s_search.bin[i] == key && s_list[i] < page);
+          s_key[page] = before < (uint32_t)a.budget ? kAlways : 0u;
+        }
+        __syncthreads();
+        threshold = kAlways - 1u;
+        need = 0;
+      } else {
+        for (int i0 = w0; i0 < w1; i0 += 32) {
+          const int i = i0 + lane;
+          const uint32_t key = i < w1 ? s_key[i] : 0u;
+          const bool mid = i < w1 && key >= low && key <= high;
+          if (i < w1 && !mid) s_key[i] = key > high ? kAlways : 0u;
+          uint32_t left = __ballot_sync(0xffffffffu, mid);
+          while (left) {
+            const int b = __ffs(left) - 1;
+            left &= left - 1u;
+            const uint32_t exact = Scores::rescore(a, p, i0 + b);
+            if (lane == 0) s_key[i0 + b] = exact;
+          }
+        }
+        __syncthreads();
+        find_threshold(s_key, held, a.budget, false, s_search, threshold, need);
+      }
     }
   }
 
   // every key above the threshold and the first `need` equal to it, in order: a
-  // stretch of pages for each warp
-  const int stretch = ((held + kWarps - 1) / kWarps + 31) & ~31;
-  const int w0 = min(warp * stretch, held), w1 = min(w0 + stretch, held);
-  uint32_t above = 0, equal = 0;
-  for (int i = w0; i < w1; i += 32) {
-    const uint32_t key = i + lane < w1 ? s_key[i + lane] : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key > threshold));
-    equal += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key == threshold));
+  // stretch of pages for each thread
+  const int mine = 4 * ((held + 4 * kThreads - 1) / (4 * kThreads));
+  const int i0 = min(tid * mine, held), i1 = min(i0 + mine, held);
+  auto each = [&](auto f) {
+    for (int i = i0; i < i1; i += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
+      f(i, k.x);
+      if (i + 1 < i1) f(i + 1, k.y);
+      if (i + 2 < i1) f(i + 2, k.z);
+      if (i + 3 < i1) f(i + 3, k.w);
+    }
+  };
+  uint32_t count = 0;  // keys above (high half) and equal (low half): at most kMaxPages of each
+  each([&](int, uint32_t key) { count += key > threshold ? 0x10000u : (key == threshold ? 1u : 0u); });
+  uint32_t up = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += x;
   }
-  __syncthreads();  // s_warp of the last pass is read
-  if (lane == 0) s_warp[warp] = above, s_warp2[warp] = equal;
+  if (lane == 31) s_count[0][warp] = up;
   __syncthreads();
-  above = equal = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w)
-    if (w < warp) above += s_warp[w], equal += s_warp2[w];
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i = w0; i < w1; i += 32) {
-    const uint32_t key = i + lane < w1 ? s_key[i + lane] : 0u;
-    const bool gt = i + lane < w1 && key > threshold, eq = i + lane < w1 && key == threshold;
-    const uint32_t gts = __ballot_sync(0xffffffffu, gt), eqs = __ballot_sync(0xffffffffu, eq);
-    const uint32_t eq_at = equal + __popc(eqs & below);
-    if (gt || (eq && eq_at < (uint32_t)need)) out[above + __popc(gts & below) + min(eq_at, (uint32_t)need)] = i + lane;
-    above += __popc(gts);
-    equal += __popc(eqs);
-  }
+    if (w < warp) up += s_count[0][w];
+  up -= count;
+  uint32_t above = up >> 16, equal = up & 0xffffu;
+  if (count != 0u)
+    each([&](int i, uint32_t key) {
+      if (key > threshold || (key == threshold && equal < (uint32_t)need)) out[above + min(equal, (uint32_t)need)] = i;
+      above += key > threshold;
+      equal += key == threshold;
+    });
 }
 
 template <typename CT, int D>
@@ -298,7 +649,7 @@ int launch_dim(const SelectArgs& a, int cluster, cudaStream_t s) {
   if (!smem_attr_once(kernel, kMaxPages * (int)sizeof(uint32_t), done)) return -1;
   prof_begin(kKSelect, s);
   const cudaError_t e = launch_chained(kernel, dim3((unsigned)((long long)a.R * a.Hkv * cluster)), kThreads,
-                                       a.max_pages * sizeof(uint32_t), cluster, s, a);
+                                       ((size_t)a.max_pages + 3) / 4 * 16, cluster, s, a);
   prof_end(kKSelect, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
 }

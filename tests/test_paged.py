@@ -203,6 +203,59 @@ def test_select_ties_go_to_the_lower_page(cp):
         assert got == sorted((top + rest)[:budget - 1] + [999])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp32"])
+@pytest.mark.parametrize("D,Hq,pages,budget", [(64, 3, 700, 100), (128, 9, 300, 20), (128, 1, 5000, 2500)])
+def test_select_near_ties_are_settled_exactly(cp, kind, D, Hq, pages, budget):
+    """Pages that differ by one step of one column, some not at all: fp32 sums could swap them."""
+    g = torch.Generator().manual_seed(pages + budget)
+    base = torch.randn(2, D, generator=g).abs() * torch.tensor([[-1.0], [1.0]])
+    b = base.expand(pages, 1, 2, D).clone()
+    col, side = torch.randint(D, (pages,), generator=g), torch.randint(2, (pages,), generator=g)
+    step = torch.where(torch.randint(3, (pages,), generator=g) > 0, 1 + 2.0 ** -7, 1.0)
+    b[torch.arange(pages), 0, side, col] *= step
+    b = b.to(torch.float8_e4m3fn).view(torch.uint8) if kind == "e4m3" else b.to(pu.DTYPES[kind])
+    q = torch.randn(1, Hq, D, generator=g).to(pu.rows_dtype(kind))
+    table = torch.randperm(pages, generator=g).int()[None]
+    n = 16 * pages - 3
+    got = cp.select_pages(q.cuda(), b.cuda(), table.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), 16, budget,
+                          keep_first=1)
+    assert cp.sync_status() == cp.OK
+    bv = pu.values(b)
+    exact = {(p, 0): (bv[p, 0, 0], bv[p, 0, 1]) for p in range(pages)}
+    # the definition's sums in 64 bits, rounded to fp32: as the oracle forms them
+    assert got.cpu().tolist()[0][0] == paged.select(pu.values(q)[0], exact, table[0], n, 16, 0, budget, 1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_select_with_infinite_and_nan_bounds(cp, kind):
+    pages, D, budget = 200, 64, 10
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn(pages, 1, 2, D, generator=g).sort(2).values
+    if kind == "bf16":
+        x[5, 0, 1, 3] = float("inf")
+        x[6, 0, 0, 3] = float("-inf")
+    x[7, 0, :, 9] = float("nan")
+    x[8, 0, 0, 9] = float("nan")
+    b = x.to(torch.float8_e4m3fn).view(torch.uint8) if kind == "e4m3" else x.to(torch.bfloat16)
+    q = torch.randn(1, 2, D, generator=g).bfloat16()
+    q[q == 0] = 1
+    q[0, 0] = q[0, 0].abs()
+    q[0, 1] = -q[0, 1].abs()
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    lens = torch.tensor([16 * pages], dtype=torch.int32)
+    got = cp.select_pages(q.cuda(), b.cuda(), table.cuda(), lens.cuda(), 16, budget).cpu().tolist()[0][0]
+    assert cp.sync_status() == cp.OK
+    bv = pu.values(b)
+    score = []
+    for j in range(pages):
+        # as the kernel writes it: min(q, 0) lo + max(q, 0) hi; a head whose sum is NaN does not count
+        heads = [np.sum(np.minimum(h, 0) * bv[j, 0, 0] + np.maximum(h, 0) * bv[j, 0, 1]) for h in pu.values(q)[0]]
+        heads = [h for h in heads if not np.isnan(h)]
+        score.append(float(np.float32(max(heads))) if heads else -np.inf)
+    score[-1] = np.inf
+    assert got == sorted(sorted(range(pages), key=lambda j: (-score[j], j))[:budget])
+
+
 def test_decode_reads_lists_with_gaps_and_pages_behind_the_length(cp):
     c = pu.make_cache([200, 70], 4, 2, 64, 16, "bf16", seed=13)
     lists = [[[-1, 3, 12, -1, 5], [12, 0, 1, 2, 3]], [[4, -1, -1, 0, 9], [9, -1, -1, -1, 2]]]
