@@ -64,6 +64,9 @@ __device__ __forceinline__ Three request_of(const PlanArgs& a, int r, int* bad) 
   return {max(0LL, after - n), max(0LL, p1 - p0), max(0LL, p0 - p1)};
 }
 
+// Place i of the ring of n entries (i < 2 n).
+__device__ __forceinline__ int ring_at(long long i, int n) { return (int)(i >= n ? i - n : i); }
+
 // One block: prefix sums over the requests, the verdict, and everything that
 // has one value per request.  Reads all lengths before it writes any, so that
 // lens_out may be lens and state_out free_state.
@@ -91,11 +94,20 @@ __device__ __forceinline__ void plan_requests(const PlanArgs& a, const Prefix& p
   const int head = a.free_state[0], count = a.free_state[1];
   __syncthreads();
   if (bad) atomicOr(&s_bad, bad);
-  Three all = {0, 0, 0};
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    if (w < warp) up.a += s_sum[w].a, up.b += s_sum[w].b, up.c += s_sum[w].c;
-    all.a += s_sum[w].a, all.b += s_sum[w].b, all.c += s_sum[w].c;
+  // every warp sums the warps' sums for itself
+  const Three part = lane < (int)(blockDim.x >> 5) ? s_sum[lane] : Three{0, 0, 0};
+  Three sums = part;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, sums.a, o), y = __shfl_up_sync(0xffffffffu, sums.b, o),
+                    z = __shfl_up_sync(0xffffffffu, sums.c, o);
+    if (lane >= o) sums.a += x, sums.b += y, sums.c += z;
   }
+  const Three all = {__shfl_sync(0xffffffffu, sums.a, 31), __shfl_sync(0xffffffffu, sums.b, 31),
+                     __shfl_sync(0xffffffffu, sums.c, 31)};
+  up.a += __shfl_sync(0xffffffffu, sums.a - part.a, warp);
+  up.b += __shfl_sync(0xffffffffu, sums.b - part.b, warp);
+  up.c += __shfl_sync(0xffffffffu, sums.c - part.c, warp);
   __syncthreads();
   int verdict = s_bad;
   if (all.b > count) verdict |= kShort;
@@ -121,7 +133,7 @@ __device__ __forceinline__ void plan_requests(const PlanArgs& a, const Prefix& p
     p.head[0] = ok;
     p.head[1] = head;
     p.head[2] = count;
-    a.state_out[0] = ok ? (int)(((long long)head + all.b) % a.num_pages) : head;
+    a.state_out[0] = ok ? ring_at(head + all.b, a.num_pages) : head;
     a.state_out[1] = ok ? (int)(count - all.b + all.c) : count;
     *a.verdict = verdict;
   }
@@ -151,7 +163,7 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
       const int pos = before + ((int)i - p.cu[r]);
       const int j = pos >> a.shift, held = (int)pages_of(before, a.shift);
       const int page = j < held ? a.table[(size_t)r * a.max_pages + j]
-                                : a.ring[((long long)head + p.pop_at[r] + (j - held)) % a.num_pages];
+                                : a.ring[ring_at((long long)head + p.pop_at[r] + (j - held), a.num_pages)];
       if (page >= 0 && page < a.num_pages)
         slot = ((long long)page << a.shift) + (pos & ((1 << a.shift) - 1));
       else
@@ -163,14 +175,15 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
   for (long long i = i0; i < pops; i += n) {
     const int r = find(p.pop_at, a.R, (int)i);
     const int held = (int)pages_of(a.lens_out[r] - a.delta[r], a.shift);
-    a.table[(size_t)r * a.max_pages + held + ((int)i - p.pop_at[r])] = a.ring[((long long)head + i) % a.num_pages];
+    a.table[(size_t)r * a.max_pages + held + ((int)i - p.pop_at[r])] =
+        a.ring[ring_at(head + i, a.num_pages)];
   }
   // returned pages go behind the last free one: count + pushes <= num_pages, so
   // none of these places is read above
   for (long long i = i0; i < pushes; i += n) {
     const int r = find(p.push_at, a.R, (int)i);
     const int left = (int)pages_of(a.lens_out[r], a.shift);
-    a.ring[((long long)head + count + i) % a.num_pages] =
+    a.ring[ring_at(ring_at((long long)head + count, a.num_pages) + i, a.num_pages)] =
         a.table[(size_t)r * a.max_pages + left + ((int)i - p.push_at[r])];
   }
 }
@@ -188,9 +201,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanA
   plan_requests(a, {a.head, a.cu, a.pop_at, a.push_at});
 }
 __global__ void __launch_bounds__(256) plan_items_kernel(const PlanArgs a) {
+  __shared__ int32_t s_at[3][kSmallR + 1];
   after_previous();
-  plan_items(a, {a.head, a.cu, a.pop_at, a.push_at}, (long long)blockIdx.x * blockDim.x + threadIdx.x,
-             (long long)gridDim.x * blockDim.x);
+  Prefix p = {a.head, a.cu, a.pop_at, a.push_at};
+  if (a.R <= kSmallR) {  // searched from shared memory: 512 requests, 80,000 tokens 4 us instead of 6
+    for (int i = threadIdx.x; i <= a.R; i += blockDim.x)
+      s_at[0][i] = a.cu[i], s_at[1][i] = a.pop_at[i], s_at[2][i] = a.push_at[i];
+    __syncthreads();
+    p.cu = s_at[0], p.pop_at = s_at[1], p.push_at = s_at[2];
+  }
+  plan_items(a, p, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
 }
 
 struct AppendArgs {
@@ -431,7 +451,7 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!need) {
     prof_begin(kKCachePlan, s);
-    const cudaError_t e = launch_chained(plan_small_kernel, dim3(1), kPlanThreads, 0, 0, s, a);
+    const cudaError_t e = launch_chained(plan_small_kernel, dim3(1), R <= 256 && capacity <= 1024 ? 256 : kPlanThreads, 0, 0, s, a);
     prof_end(kKCachePlan, s);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
     add_launches(1);
