@@ -75,11 +75,34 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ void store_o(const DecodeArgs& a, size_t i, float x) {
-  if (a.o_bf16)
-    static_cast<__nv_bfloat16*>(a.o)[i] = __float2bfloat16_rn(x);
-  else
-    static_cast<float*>(a.o)[i] = x;
+// outputs i .. i + N - 1 (N = 2 or 4, i a multiple of N)
+template <int N>
+__device__ __forceinline__ void store_o(const DecodeArgs& a, size_t i, const float (&x)[N]) {
+  if (a.o_bf16) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      w[e] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    void* to = static_cast<__nv_bfloat16*>(a.o) + i;
+    if constexpr (N == 4) *static_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+    else *static_cast<uint32_t*>(to) = w[0];
+  } else {
+    void* to = static_cast<float*>(a.o) + i;
+    if constexpr (N == 4) *static_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+    else *static_cast<float2*>(to) = make_float2(x[0], x[1]);
+  }
+}
+// A head's weighted sum and sum of weights (reference m) as the output and the
+// log-sum-exp.  A head without a key: o = 0, lse = -inf.
+template <int N>
+__device__ __forceinline__ void finish(const DecodeArgs& a, size_t out, int D, int d, float (&o)[N], float m, float l) {
+  const float f = l == 0.f ? 0.f : __frcp_rn(l);
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] *= f;
+  store_o<N>(a, out * D + d, o);
+  if (d == 0) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // One warp's view of 16 keys in shared memory.  Lane 4g + t holds, for every 8
@@ -431,13 +454,15 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
   // the warps' rings of K and V blocks; between pairs, when nothing is under way, the warps' outputs
   extern __shared__ char s_raw[];
   char* s_ring = s_raw + ((1024u - (sm100::smem_u32(s_raw) & 1023u)) & 1023u);
-  float(*s_buf)[D] = reinterpret_cast<float(*)[D]>(s_ring);
+  constexpr int kRow = D + 4;  // of the outputs: the lanes' 16 bytes fall into different banks
+  float(*s_buf)[kRow] = reinterpret_cast<float(*)[kRow]>(s_ring);
+  static_assert(kWarps * HT * kRow * 4 <= kWarps * kDepth * SUB * 2 * kBlock, "the outputs fit into the rings");
   __shared__ __align__(16) char s_queries[kGroups * HT * Tile::kQueryBytes];
   __shared__ __align__(8) uint64_t s_full[kWarps][kDepth];
   __shared__ int s_valid[kWarps][kDepth][SUB], s_abort;
   __shared__ float s_unit[kGroups * HT];
   __shared__ float s_m[kWarps][HT], s_l[kWarps][HT];
-  __shared__ long long s_scan[kWarps], s_base;
+  __shared__ int s_scan[kWarps], s_base;
   __shared__ int s_r;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -457,42 +482,43 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
     if (request_units<UNIT>(a, request_len(a, r, tid == 0)) != 0) continue;
     if (a.by_pair)
       for (int h = tid; h < a.Hkv; h += kThreads) a.tail[r * a.Hkv + h] = make_int4(-1, 0, 0, 0);
-    for (int i = tid; i < a.Hq * D; i += kThreads) store_o(a, (size_t)r * a.Hq * D + i, 0.f);
+    const float none[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 4 * tid; i < a.Hq * D; i += 4 * kThreads) store_o<4>(a, (size_t)r * a.Hq * D + i, none);
     for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)r * a.Hq + i] = -INFINITY;
   }
 
   // this block's share of the line
-  auto weight = [&](int r) { return (long long)pair_weight(request_units<UNIT>(a, request_len(a, r, false))) * a.Hkv; };
+  auto weight = [&](int r) { return pair_weight(request_units<UNIT>(a, request_len(a, r, false))) * a.Hkv; };
   const int per = (a.R + kThreads - 1) / kThreads;
   const int r_lo = min(tid * per, a.R), r_hi = min(r_lo + per, a.R);
-  long long mine = 0;
+  int mine = 0;
   for (int r = r_lo; r < r_hi; ++r) mine += weight(r);
-  long long upto = mine;
+  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += x;
   }
   if (lane == 31) s_scan[warp] = upto;
   __syncthreads();
-  long long total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) upto += s_scan[w];
     total += s_scan[w];
   }
-  const long long n_cta = min((long long)gridDim.x, total);
-  long long u = 0, u_end = 0;
-  if (cta < n_cta) u = total * cta / n_cta, u_end = total * (cta + 1) / n_cta;
+  // `each` units for every block and one more for the first `more`
+  const int n_cta = max(1, min((int)gridDim.x, total)), each = total / n_cta, more = total - each * n_cta;
+  int u = each * cta + min(cta, more);
+  const int u_end = cta < n_cta ? u + each + (cta < more ? 1 : 0) : u;
   if (u >= u_end) {
     if (tid == 0 && !a.by_pair) a.tail[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
   if (upto - mine <= u && u < upto) {  // one thread's requests hold the first unit
-    long long base = upto - mine;
-    int r = r_lo;
+    int base = upto - mine, r = r_lo;
     for (;; ++r) {
-      const long long n = weight(r);
+      const int n = weight(r);
       if (u < base + n) break;
       base += n;
     }
@@ -500,8 +526,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
     s_base = base;
   }
   __syncthreads();
-  int r = s_r;
-  long long base = s_base;
+  int r = s_r, base = s_base;
 
   const int hgroups = a.group <= HT ? 1 : (a.group <= 2 * HT ? 2 : 4);  // head groups: warps share keys
   const int kwarps = kWarps / hgroups;
@@ -515,13 +540,13 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
   while (u < u_end) {
     const int len = request_len(a, r, false);
     const int n_units = request_units<UNIT>(a, len), w_pair = pair_weight(n_units);
-    if (u >= base + (long long)w_pair * a.Hkv) {
-      base += (long long)w_pair * a.Hkv;
+    if (u >= base + w_pair * a.Hkv) {
+      base += w_pair * a.Hkv;
       ++r;
       continue;
     }
-    const int h = (int)((u - base) / w_pair), y0 = (int)((u - base) % w_pair);
-    const int y1 = (int)min((long long)w_pair, y0 + (u_end - u));
+    const int h = (u - base) / w_pair, y0 = u - base - h * w_pair;
+    const int y1 = min(w_pair, y0 + (u_end - u));
     u += y1 - y0;
     // the pair's own cost stands before its units
     const int x0 = max(0, y0 - kPairCost), x1 = max(0, y1 - kPairCost);
@@ -692,37 +717,38 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
 #pragma unroll
         for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s_buf[warp * HT + head][Tile::col(hh, g, e)] = acc[nt][hh][2 * e + i];
+          for (int e = 0; e < 8; e += 4)
+            *reinterpret_cast<float4*>(&s_buf[warp * HT + head][Tile::col(hh, g, e)]) =
+                make_float4(acc[nt][hh][2 * e + i], acc[nt][hh][2 * e + 2 + i], acc[nt][hh][2 * e + 4 + i], acc[nt][hh][2 * e + 6 + i]);
       }
     __syncthreads();
     const bool whole = x0 == 0 && x1 == n_units;
     const int slot = 2 * cta + (x0 == 0 ? 1 : 0);
-    for (int i = tid; i < a.group * D; i += kThreads) {
-      const int head = i / D, d = i % D, hw = head / HT, hh = head % HT;
-      float mm = kNothing, ll = 0.f, oo = 0.f;
-      for (int w = 0; w < kwarps; ++w) mm = fmaxf(mm, s_m[w * hgroups + hw][hh]);
-      for (int w = 0; w < kwarps; ++w) {
-        const float f = exp2_fast(s_m[w * hgroups + hw][hh] - mm);
-        ll = fmaf(f, s_l[w * hgroups + hw][hh], ll);
-        oo = fmaf(f, s_buf[(w * hgroups + hw) * HT + hh][d], oo);
+    for (int i = tid; i < a.group * (D / 4); i += kThreads) {
+      const int head = i / (D / 4), d = i % (D / 4) * 4, hw = head / HT, hh = head % HT;
+      float mm = kNothing, ll = 0.f, oo[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w = hw; w < kWarps; w += hgroups) mm = fmaxf(mm, s_m[w][hh]);
+      for (int w = hw; w < kWarps; w += hgroups) {
+        const float f = exp2_fast(s_m[w][hh] - mm);
+        const float4 x = *reinterpret_cast<const float4*>(&s_buf[w * HT + hh][d]);
+        ll = fmaf(f, s_l[w][hh], ll);
+        oo[0] = fmaf(f, x.x, oo[0]), oo[1] = fmaf(f, x.y, oo[1]), oo[2] = fmaf(f, x.z, oo[2]), oo[3] = fmaf(f, x.w, oo[3]);
       }
-      oo *= v_unit;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) oo[e] *= v_unit;
       if (whole) {
-        const size_t out = (size_t)r * a.Hq + (size_t)h * a.group + head;
-        store_o(a, out * D + d, ll == 0.f ? 0.f : oo / ll);
-        if (d == 0) a.lse[out] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+        finish<4>(a, (size_t)r * a.Hq + (size_t)h * a.group + head, D, d, oo, mm, ll);
       } else {
-        a.part_o[((size_t)slot * a.group + head) * D + d] = oo;
-        if (d == 0) {
-          a.part_ml[((size_t)slot * a.group + head) * 2] = mm;
-          a.part_ml[((size_t)slot * a.group + head) * 2 + 1] = ll;
-        }
+        const size_t at = (size_t)slot * a.group + head;
+        *reinterpret_cast<float4*>(a.part_o + at * D + d) = make_float4(oo[0], oo[1], oo[2], oo[3]);
+        if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mm, ll);
       }
     }
     if (x0 == 0) {
-      // the block that holds the pair's last unit: the largest c with total * c / n_cta <= last
-      const long long last = base + (long long)(h + 1) * w_pair - 1;
-      if (!whole) tail = make_int4(r, h, (int)(((last + 1) * n_cta - 1) / total), cta);
+      if (!whole) {  // the block that holds the pair's last unit
+        const int last = base + (h + 1) * w_pair - 1, long_ones = more * (each + 1);
+        tail = make_int4(r, h, last < long_ones ? last / (each + 1) : more + (last - long_ones) / each, cta);
+      }
       if (tid == 0 && a.by_pair) a.tail[r * a.Hkv + h] = whole ? make_int4(-1, 0, 0, 0) : tail;
     }
   }
@@ -797,10 +823,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const DecodeArgs 
 #pragma unroll
       for (int e = 0; e < V; ++e) oo[e] = fmaf(f, s_o[warp + w][lane * V + e], oo[e]);
     }
-    const size_t out = (size_t)tail.x * a.Hq + (size_t)tail.y * a.group + head;
-#pragma unroll
-    for (int e = 0; e < V; ++e) store_o(a, out * D + lane * V + e, ll == 0.f ? 0.f : oo[e] / ll);
-    if (lane == 0) a.lse[out] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+    finish<V>(a, (size_t)tail.x * a.Hq + (size_t)tail.y * a.group + head, D, lane * V, oo, mm, ll);
   }
 }
 
@@ -933,6 +956,7 @@ int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,
   const long long listed = pages ? std::min(budget, max_pages) : max_pages;
   const long long max_units = (long long)R * Hkv * (((listed << shift) + kWarps * kChunk - 1) / (kWarps * kChunk) + kPairCost);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (max_units > 0x7fffffffLL) return CPATTN_ERR_SHAPE;
   char* ws = static_cast<char*>(workspace);
   const int n = D == 64 ? launch_decode<64>(a, cache_dtype, s, max_units, ws)
                         : launch_decode<128>(a, cache_dtype, s, max_units, ws);
