@@ -395,13 +395,15 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
  * cpattn_cache_append -- rows k_new[i][h][:], v_new[i][h][:] (i < N, h < Hkv) into
  * slots[i] of the cache; negative slots are skipped.
  *   strides        of tokens and heads in elements, multiples of 16 bytes
- *                  (CPATTN_ERR_SHAPE); columns are contiguous.  K and V as the layer
+ *                  (CPATTN_ERR_SHAPE; not looked at for one token or one head);
+ *                  columns are contiguous.  K and V as the layer
  *                  saves them ([H][S][D]) have token stride D and head stride S * D
  *   k_bounds       kept up to date, or NULL.  A row in a page's first slot starts
  *                  the page's bounds afresh.  With k_bounds, the new tokens of one
  *                  page must stand next to one another and ascend, as
  *                  cpattn_cache_plan lists them.  Bounds do not shrink when tokens are
- *                  taken back: they still cover the rows that were there
+ *                  taken back: they still cover the rows that were there.  NaN
+ *                  keys are left out of them
  * A slot may appear once only.  N = 0 does nothing.
  */
 int cpattn_cache_append(const void* k_new, const void* v_new, long k_tok_stride, long k_head_stride,
@@ -475,8 +477,8 @@ const char* cpattn_status_str(int status);
  *   setting.  For tests that compare the kernel families.
  * cpattn_last_path: kernel family used by the last fwd/bwd call
  *   (0 tcgen05, 1 CUDA cores).
- * cpattn_debug_stall: n > 0 makes the next n tcgen05 forward launches omit one
- *   K/V tile load, so the bounded waits run out and the call reports
+ * cpattn_debug_stall: n > 0 makes the next n tcgen05 forward or cpattn_decode
+ *   launches omit one K/V load, so the bounded waits run out and the call reports
  *   CPATTN_ERR_TIMEOUT through cpattn_sync_status; the device stays usable.
  *   For failure-detection tests only.
  */

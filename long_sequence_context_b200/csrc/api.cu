@@ -99,6 +99,13 @@ int check_attention_shape(int B, int H, int S, int D, int cp_size, int causal, f
 void add_launches(int n) { g_launches += n; }
 
 unsigned* device_error_word() { return err_word(); }
+
+int take_stall() {
+  int cur = g_stall.load();
+  while (cur > 0 && !g_stall.compare_exchange_weak(cur, cur - 1)) {
+  }
+  return cur > 0 ? 1 : 0;
+}
 int kernel_path() { return g_path.load(); }
 }  // namespace cpattn
 
@@ -174,11 +181,7 @@ int cpattn_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
   if (!err) return CPATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (use_tc_fwd(sh)) {
-    int stall = 0;
-    int cur = g_stall.load();
-    while (cur > 0 && !g_stall.compare_exchange_weak(cur, cur - 1)) {
-    }
-    if (cur > 0) stall = 1;
+    const int stall = take_stall();
     g_last_path = 0;
     return count(launch_tc_fwd(sh, q, k, v, o, lse, err, stall, s));
   }

@@ -42,7 +42,7 @@ struct DecodeArgs {
   unsigned* err;
   int R, Hq, Hkv, group, shift, max_pages, num_pages, budget;
   float scale_log2;
-  int o_bf16;
+  int o_bf16, stall;
 };
 
 // Keys of request r in the order its page list gives them (whole pages where
@@ -591,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
         s_valid[warp][slot][sub] = valid;
         if (valid > 0 && !s_abort) {
           sm100::mbar_expect_tx(&s_full[warp][slot], 2 * kBlock);
-          sm100::tma_load_2d(to, &k_map, &s_full[warp][slot], 0, line);
+          if (!(a.stall && base + h + x0 + warp + i == 0))  // else: failure-detection tests only
+            sm100::tma_load_2d(to, &k_map, &s_full[warp][slot], 0, line);
           sm100::tma_load_2d(to + kBlock, &v_map, &s_full[warp][slot], 0, line);
         } else {
           sm100::mbar_arrive(&s_full[warp][slot]);
@@ -953,6 +954,7 @@ int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,
   a.budget = budget;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o_bf16 = o_dtype == CPATTN_BF16;
+  a.stall = take_stall();
   const long long listed = pages ? std::min(budget, max_pages) : max_pages;
   const long long max_units = (long long)R * Hkv * (((listed << shift) + kWarps * kChunk - 1) / (kWarps * kChunk) + kPairCost);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

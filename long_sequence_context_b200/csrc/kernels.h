@@ -64,6 +64,9 @@ int num_sms(int device);
 // once per device), or null when the lookup failed.
 unsigned* device_error_word();
 
+// 1 when cpattn_debug_stall asks this launch to omit a load (taken once), else 0.
+int take_stall();
+
 // Kernel family selected by cpattn_set_path: 0 automatic, 1 CUDA cores only,
 // 2 tcgen05 kernels on one SM each (no two-SM kernels).
 int kernel_path();

@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       for (int i = 0; i < 8; ++i) norm = fmaxf(norm, s_norm[i]);
       for (int i = 0; i < ranks; ++i) most = fmaxf(most, s_most[i]);
       const float at = key_value(threshold);
-      const float eps = norm * most * ((D / 2 + 2) * 0x1p-23f) * 1.01f + fabsf(at) * 0x1p-22f;
+      // the last term: products and operands below the normal range
+      const float eps = norm * most * ((D / 2 + 2) * 0x1p-23f) * 1.01f + fabsf(at) * 0x1p-22f +
+                        2 * D * 0x1p-126f * (norm + most + 1.f);
       uint32_t low = 0u, high = kAlways - 1u;
       if (threshold != 0u && eps < 1e37f && fabsf(at) < 1e37f)
         low = order_key(__fadd_rd(at, -2.f * eps)), high = min(high, order_key(__fadd_ru(at, 2.f * eps)));

@@ -1,4 +1,8 @@
 """The paged key-value cache on the GPU against the fp64 oracle."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -495,3 +499,109 @@ def test_two_streams_with_their_own_workspaces(cp):
         ref = pu.reference(cs[i], 128 ** -0.5)
         for o, lse in got[i]:
             pu.assert_decode(o, lse, ref, 128, 128 ** -0.5, 2001, "bf16")
+
+
+def test_ordinary_calls_and_calls_through_ctypes_agree(cp, monkeypatch):
+    c = pu.on_gpu(pu.make_cache([300, 0, 41], 6, 2, 64, 16, "e4m3", seed=40))
+    g = torch.Generator().manual_seed(41)
+    rows = torch.randn(5, 2, 64, generator=g).bfloat16().cuda()
+    slots = torch.tensor([3, 4, -1, 20, 21], device="cuda")
+    bounds = torch.randn(c["k"].shape[0], 2, 2, 64, generator=g).sort(2).values.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    s = _books(3, 4, 9)
+    delta = torch.tensor([20, 0, 33], dtype=torch.int32, device="cuda")
+
+    def all_four():
+        k, v, b = c["k"].clone(), c["v"].clone(), bounds.clone()
+        table, ring = s["table"].clone(), s["ring"].clone()
+        out = list(cp.cache_plan(s["lens"], delta, table, ring, s["state"], 16, 60)) + [table, ring]
+        cp.cache_append_(rows, rows, slots, k, v, k_bounds=b, kv_amax=c["amax"])
+        pages = cp.select_pages(c["q"], b, c["table"], c["lens"], 16, 5, keep_first=1)
+        out += [k, v, b, pages, *cp.decode(c["q"], k, v, c["table"], c["lens"], pages=pages, kv_amax=c["amax"], scale=0.2)]
+        return out
+
+    first = all_four()
+    for name in ("cache_plan", "cache_append", "select_pages", "decode"):
+        monkeypatch.setattr(cp._calls, name, lambda *a: None)
+    second = all_four()
+    assert cp.sync_status() == cp.OK
+    assert len(first) == len(second) and all(torch.equal(x, y) for x, y in zip(first, second))
+
+
+def test_ordinary_calls_raise_the_library_s_errors(cp):
+    c = pu.on_gpu(pu.make_cache([30], 2, 1, 64, 16, "bf16", seed=42))
+    args = (c["q"], c["k"], c["v"], c["table"], c["lens"])
+    with pytest.raises(cp.CpattnError) as e:
+        cp.decode(*args, scale=-1.0)
+    assert e.value.status == cp.ERR_ARG
+    with pytest.raises(cp.CpattnError) as e:  # a page of 24 rows
+        cp.decode(c["q"], c["k"].new_zeros(2, 1, 24, 64), c["k"].new_zeros(2, 1, 24, 64), c["table"], c["lens"])
+    assert e.value.status == cp.ERR_SHAPE
+    x = torch.zeros(3 * 64 + 4, dtype=torch.bfloat16, device="cuda")
+    off = x[4:].view(3, 1, 64)  # 8 bytes behind an aligned address
+    with pytest.raises(cp.CpattnError) as e:
+        cp.cache_append_(off, off, torch.arange(3, device="cuda"), c["k"], c["v"])
+    assert e.value.status == cp.ERR_ALIGN
+    assert cp.sync_status() == cp.OK
+
+
+def test_append_of_one_token_with_any_stride_of_the_token_axis(cp):
+    k = torch.zeros((2, 3, 16, 64), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    x = torch.randn(3, 64, 1, device="cuda").bfloat16().permute(2, 0, 1)
+    assert x.stride(0) == 1
+    cp.cache_append_(x, x, torch.tensor([19], device="cuda"), k, v)
+    assert cp.sync_status() == cp.OK and torch.equal(k[1, :, 3], x[0])
+    assert k.count_nonzero() == x.count_nonzero()
+
+
+def test_decode_wait_that_runs_out_is_reported_and_the_device_stays_usable(cp):
+    """One block's load is left out: its wait gives up after its limit, the call ends."""
+    c = pu.make_cache([900, 70], 4, 2, 64, 32, "bf16", seed=43)
+    assert cp.sync_status() == cp.OK
+    cp.debug_stall(1)
+    try:
+        d = pu.on_gpu(c)
+        cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"])
+        st = cp.sync_status()
+    finally:
+        cp.debug_stall(0)
+    assert st == cp.ERR_TIMEOUT, cp.status_str(st)
+    o, lse = _decode(cp, c, 0.125)
+    pu.assert_decode(o, lse, pu.reference(c, 0.125), 64, 0.125, 900, "bf16", "after it")
+
+
+def test_select_with_operands_below_the_normal_range(cp):
+    pages, D = 100, 64
+    g = torch.Generator().manual_seed(44)
+    b = (torch.randn(pages, 1, 2, D, generator=g).sort(2).values).bfloat16()
+    q = (torch.randn(1, 1, D, generator=g) * 1e-39).bfloat16()
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    got = cp.select_pages(q.cuda(), b.cuda(), table.cuda(), torch.tensor([16 * pages], dtype=torch.int32, device="cuda"), 16, 9)
+    bv = pu.values(b)
+    want = paged.select(pu.values(q)[0], {(p, 0): (bv[p, 0, 0], bv[p, 0, 1]) for p in range(pages)}, table[0], 16 * pages, 16, 0, 9, 0)
+    assert got.cpu().tolist()[0][0] == want
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """No call has gone before in the child: module loading and attributes fall into the capture."""
+    code = (
+        "import torch\n"
+        "from long_sequence_context_b200 import cpattn as cp\n"
+        "z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device='cuda')\n"
+        "k, q = z(4, 1, 16, 64, t=torch.bfloat16), z(1, 2, 64, t=torch.bfloat16)\n"
+        "b, lens, table, ring = z(4, 1, 2, 64, t=torch.bfloat16), z(1), z(1, 3), torch.arange(4, dtype=torch.int32, device='cuda')\n"
+        "state, delta, x = torch.tensor([0, 4], dtype=torch.int32, device='cuda'), z(1) + 40, z(40, 1, 64, t=torch.bfloat16) + 1\n"
+        "torch.cuda.synchronize()\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    n, _, cu, slots, verdict = cp.cache_plan(lens, delta, table, ring, state, 16, 40)\n"
+        "    cp.cache_append_(x, x, slots, k, k, k_bounds=b)\n"
+        "    pages = cp.select_pages(q, b, table, n, 16, 2)\n"
+        "    o, lse = cp.decode(q, k, k, table, n, pages=pages)\n"
+        "g.replay()\n"
+        "cp.check_device_status()\n"
+        "assert verdict.item() == 0 and n.item() == 40 and pages.tolist() == [[[0, 2]]], (verdict, n, pages)\n"
+        "assert torch.all(o == 1) and abs(lse[0, 0].item() - __import__('math').log(24)) < 1e-6\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stdout + r.stderr
