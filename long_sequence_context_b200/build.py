@@ -65,7 +65,7 @@ def _build_calls(force):
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
            "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(cuda, "include"),
            "-I", sysconfig.get_paths()["include"], src, "-o", CALLS + ".tmp", "-L", os.path.join(torch_dir, "lib"),
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -12,7 +12,7 @@
 // (bind), so that both ways call the same loaded library.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -53,7 +53,7 @@ bool fits_int(long long x) { return x >= 0 && x <= 0x7fffffffLL; }
 bool current(int dev) { return c10::cuda::current_device() == dev; }
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 at::Tensor empty(std::initializer_list<int64_t> sizes, at::ScalarType type, int dev) {
-  return at::empty(sizes, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev)));
+  return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
 }
 PyObject* answer(int status, std::initializer_list<at::Tensor> outputs) {
   PyObject* r = PyTuple_New((Py_ssize_t)outputs.size() + 1);
