@@ -382,7 +382,7 @@ enum {
  * Pages returned by a call can be taken from the next call on.
  * Workspace: cpattn_cache_plan_workspace_bytes(R, capacity), 16-byte aligned;
  * contents on entry are ignored; calls that can overlap on the GPU need one each.
- * 0 (and NULL) for steps of up to 1024 requests and 4096 tokens.
+ * 0 (and NULL) for steps of up to 1024 requests and 2048 tokens.
  */
 size_t cpattn_cache_plan_workspace_bytes(int R, long capacity);
 int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_table, int R,

@@ -7,10 +7,15 @@
 // (request, kv head) pairs, with kPairCost more for each pair, form one line,
 // which is dealt to the thread blocks in equal contiguous shares: a block finds
 // its share from the lengths alone, on the device, so that a batch of very
-// different lengths keeps every block equally busy and the host needs no length.  A pair that lies inside one block is
-// finished there; the others leave one partial result (running maximum, sum,
-// unnormalised output, all fp32) per block, and join_kernel combines them by
-// the log-sum-exp rule of cpattn_merge.
+// different lengths keeps every block equally busy and the host needs no length.
+// A pair that lies inside one block is finished there; the others leave one
+// partial result (running maximum, sum, unnormalised output, all fp32) per block,
+// and join_kernel combines them by the log-sum-exp rule of cpattn_merge.
+//
+// What bounds it: K and V are read once, for up to 16 heads a group at 80 to 98%
+// of a plain copy's bandwidth (32768 keys x 32 heads x 128 bf16: 537 MB in 85 us,
+// 6.3 TB/s), beside some 6 us of start, partial results and join, which is what
+// short contexts take.
 #include <algorithm>
 
 #include "cpattn.h"
@@ -27,8 +32,11 @@ using namespace paged;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kNothing = -3.0e38f;  // the running maximum before any key: finite, so that no difference is inf - inf
-constexpr int kChunk = 16;   // keys of one tile; never straddles pages
-constexpr int kPairCost = 4;  // what starting and finishing a pair costs, in units of keys
+constexpr int kChunk = 16;  // keys of one block; never straddles pages
+// What starting and finishing a pair costs, in units of keys: without it a block
+// that draws many short pairs ends last (48 requests of 1 to 16384 keys: 97 us with
+// 0, 67.5 with 2, 66 to 66.6 with 3 to 8).
+constexpr int kPairCost = 4;
 constexpr int kMaxGroup = 64;
 
 struct DecodeArgs {
@@ -252,9 +260,13 @@ struct MmaTile {
   static constexpr bool kHalf = sizeof(C) == 1;
   static constexpr int kQueryBytes = D * 2;
   static constexpr int kRowBytes = D * (int)sizeof(C);  // 256, 128 or 64
-  static constexpr int kSub = 256 / kRowBytes;          // 8 KB of K and V at a time, 16 under way
+  // 8 KB of K and V at a time and twice that under way for each warp, 128 KB for an SM.
+  // Measured (32768 keys x 32 heads bf16; 131072 x 8 e4m3, us): as here 84.6, 51.0; three
+  // blocks of an SM 86.4, 53.0 (more partial results); three deep 87.5, 53.2; one block
+  // six deep 88.0, 65.2; e4m3 in steps of 16 keys, four deep, 54.3.
+  static constexpr int kSub = 256 / kRowBytes;
   static constexpr int kDepth = 2;
-  static constexpr int kCtas = NT == 1 ? 3 : 2;
+  static constexpr int kCtas = 2;
   // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
   // ends at 2^-24, which must be far below the largest weight of a long context.
   static constexpr float kLift = kHalf ? 14.f : 0.f, kSlack = kHalf ? 1.f : 8.f;
@@ -842,7 +854,7 @@ bool sizes_ok(int R, int Hq, int Hkv, int D) {
 // bytes of the workspace of a grid: partial outputs, (maximum, sum) pairs, tails
 size_t ws_part_o(int grid, int group, int D) { return (size_t)2 * grid * group * D * sizeof(float); }
 size_t ws_part_ml(int grid, int group) { return ((size_t)2 * grid * group * 2 * sizeof(float) + 15) & ~(size_t)15; }
-constexpr int kMostCtas = 4;  // blocks of an SM, over all variants
+constexpr int kMostCtas = 3;  // blocks of an SM, over all variants
 
 template <typename Tile, int D, int NT>
 int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
@@ -877,7 +889,9 @@ int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
 
 template <int D>
 int launch_decode(const DecodeArgs& a, int cache_dtype, cudaStream_t s, long long max_units, char* ws) {
-  const bool one = a.group <= 8;  // head tiles of a warp
+  // One tile of 8 heads for a warp, or two: a group of 8 in two tiles takes 54 to 59 us
+  // (e4m3) and 63 to 136 (fp32) for 268 MB, and as long in bf16.
+  const bool one = a.group <= 8;
   switch (cache_dtype) {
     case CPATTN_BF16:
       return one ? launch_tile<MmaTile<__nv_bfloat16, D, 1>, D, 1>(a, s, max_units, ws)
