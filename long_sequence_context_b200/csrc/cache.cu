@@ -176,20 +176,43 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
     a.slots[i] = slot;
   }
   if (!ok) return;
-  for (long long i = i0; i < pops; i += n) {
-    const int r = find(p.pop_at, a.R, (int)i);
-    const int held = (int)pages_of(a.lens_out[r] - a.delta[r], a.shift);
-    a.table[(size_t)r * a.max_pages + held + ((int)i - p.pop_at[r])] =
-        a.ring[ring_at(head + i, a.num_pages)];
-  }
-  // returned pages go behind the last free one: count + pushes <= num_pages, so
-  // none of these places is read above
-  for (long long i = i0; i < pushes; i += n) {
-    const int r = find(p.push_at, a.R, (int)i);
-    const int left = (int)pages_of(a.lens_out[r], a.shift);
-    a.ring[ring_at(ring_at((long long)head + count, a.num_pages) + i, a.num_pages)] =
-        a.table[(size_t)r * a.max_pages + left + ((int)i - p.push_at[r])];
-  }
+  // Returned pages go behind the last free one: count + pushes <= num_pages, so none of
+  // these places is read.
+  auto find_page = [&](int k, const int32_t* at, bool back, size_t& cell, int& place) {
+    const int r = find(at, a.R, k);
+    const int first = (int)pages_of(back ? a.lens_out[r] : a.lens_out[r] - a.delta[r], a.shift);
+    cell = (size_t)r * a.max_pages + first + (k - at[r]);
+    place = ring_at((back ? ring_at((long long)head + count, a.num_pages) : head) + (long long)k, a.num_pages);
+  };
+  auto move = [&](int total, const int32_t* at, bool back) {
+    // several at a time while there are: one block may have to return the pages of a long context
+    constexpr int kAhead = 4;
+    long long i = i0;
+#pragma unroll 1
+    for (; i + (kAhead - 1) * n < total; i += kAhead * n) {
+      size_t cell[kAhead];
+      int place[kAhead], page[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) find_page((int)(i + x * n), at, back, cell[x], place[x]);
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) page[x] = back ? a.table[cell[x]] : a.ring[place[x]];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (back) a.ring[place[x]] = page[x];
+        else a.table[cell[x]] = page[x];
+      }
+    }
+#pragma unroll 1
+    for (; i < total; i += n) {
+      size_t cell;
+      int place;
+      find_page((int)i, at, back, cell, place);
+      if (back) a.ring[place] = a.table[cell];
+      else a.table[cell] = a.ring[place];
+    }
+  };
+  move(pops, p.pop_at, false);
+  move(pushes, p.push_at, true);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const PlanArgs a) {

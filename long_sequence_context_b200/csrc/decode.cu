@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
   }
   if (upto - mine <= u && u < upto) {  // one thread's requests hold the first unit
     int base = upto - mine, r = r_lo;
-    for (;; ++r) {
+    for (; r < r_hi - 1; ++r) {
       const int n = weight(r);
       if (u < base + n) break;
       base += n;
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
     const int n_units = request_units<UNIT>(a, len), w_pair = pair_weight(n_units);
     if (u >= base + w_pair * a.Hkv) {
       base += w_pair * a.Hkv;
-      ++r;
+      if (++r >= a.R) break;  // not with lengths that stand still
       continue;
     }
     const int h = (u - base) / w_pair, y0 = u - base - h * w_pair;

@@ -310,6 +310,18 @@ def test_plan_steps_match_oracle(cp, R, width, P, num_pages, most, cap):
         s, _, _, _ = _plan(cp, s, delta, P, cap)
 
 
+def test_plan_returns_and_takes_thousands_of_pages_in_a_small_step(cp):
+    """One token for one request while another returns 5000 pages and a third takes 900."""
+    P, width = 16, 5200
+    s = _books(3, width, 7000, head=6990, seed=8)
+    s, _, _, v = _plan(cp, s, [80000, 100, 3], P, 80103)
+    assert v == 0
+    s, _, slots, v = _plan(cp, s, [-80000, 1, 1000], P, 1001)
+    assert v == 0 and slots[:1001].min() >= 0
+    s, _, _, v = _plan(cp, s, [1, -101, -1003], P, 1)
+    assert v == 0 and s["state"][1].item() == 6999
+
+
 def test_plan_refusals_change_nothing(cp):
     s, _, _, v = _plan(cp, _books(3, 4, 9), [20, 33, 5], 16, 64)
     assert v == 0
