@@ -59,6 +59,16 @@ def test_decode_long_context_split_over_many_blocks(cp, kind, D, P, Hkv):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp32"])
+@pytest.mark.parametrize("group,D", [(17, 128), (32, 64), (48, 128), (64, 64)])
+def test_decode_large_groups_over_long_and_short_requests(cp, kind, group, D):
+    """Warps of several head groups share the keys' ring, over many pairs and turns."""
+    lens = [5003, 0, 64, 1, 900, 2048, 17]
+    c = pu.make_cache(lens, 2 * group, 2, D, 64, kind, seed=group + D)
+    o, lse = _decode(cp, c, D ** -0.5)
+    pu.assert_decode(o, lse, pu.reference(c, D ** -0.5), D, D ** -0.5, max(lens), kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp32"])
 def test_decode_many_short_requests(cp, kind):
     g = np.random.default_rng(6)
     lens = [int(x) for x in g.integers(0, 40, 700)]
@@ -566,9 +576,10 @@ def test_append_of_one_token_with_any_stride_of_the_token_axis(cp):
     assert k.count_nonzero() == x.count_nonzero()
 
 
-def test_decode_wait_that_runs_out_is_reported_and_the_device_stays_usable(cp):
+@pytest.mark.parametrize("heads", [4, 64])
+def test_decode_wait_that_runs_out_is_reported_and_the_device_stays_usable(cp, heads):
     """One block's load is left out: its wait gives up after its limit, the call ends."""
-    c = pu.make_cache([900, 70], 4, 2, 64, 32, "bf16", seed=43)
+    c = pu.make_cache([900, 70], heads, 2, 64, 32, "bf16", seed=43)
     assert cp.sync_status() == cp.OK
     cp.debug_stall(1)
     try:
