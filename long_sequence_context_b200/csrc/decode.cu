@@ -12,10 +12,14 @@
 // partial result (running maximum, sum, unnormalised output, all fp32) per block,
 // and join_kernel combines them by the log-sum-exp rule of cpattn_merge.
 //
-// What bounds it: K and V are read once, for up to 16 heads a group at 80 to 98%
-// of a plain copy's bandwidth (32768 keys x 32 heads x 128 bf16: 537 MB in 85 us,
-// 6.3 TB/s), beside some 6 us of start, partial results and join, which is what
-// short contexts take.
+// What bounds it: K and V are read once, in bf16 and for up to 16 heads a group at
+// 93 to 99% of a plain copy's bandwidth (32768 keys x 32 heads x 128: 537 MB in 84
+// us, 6.4 TB/s; 131072 x 8 heads in e4m3, where the codes' widening doubles the
+// instructions for a byte: 268 MB in 51 us), beside some 6 us of start, partial
+// results and join, which is what short contexts take.  Groups of 32 heads wait for
+// their instructions (268 MB in 70 us); sharing a ring between the warps of a group
+// took longer (77), and so did fewer blocks with more units each (257 keys x 16
+// heads: one unit a block 6.9 us, two 7.3, four 8.6).
 #include <algorithm>
 
 #include "cpattn.h"

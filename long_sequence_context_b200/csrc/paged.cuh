@@ -9,7 +9,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -27,9 +26,7 @@ struct E4m3 {
   uint8_t code;
 };
 
-constexpr int kMinPage = 16;
-constexpr int kMaxPage = 256;
-
+// log2 of a page size, or -1 for one that is not supported
 inline int page_shift(int page_size) {
   for (int s = 4; s <= 8; ++s)
     if (page_size == (1 << s)) return s;
@@ -88,7 +85,7 @@ __device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// N consecutive stored elements (4 * N / 4 ... bytes already in registers) as floats
+// the elements of a 32-bit word as floats
 template <typename CT>
 struct Unpack;
 template <>

@@ -86,6 +86,29 @@ def test_decode_large_scores(cp, kind):
     pu.assert_decode(o, lse, ref, 128, 8.0, 777, kind)
 
 
+def test_a_batch_of_twenty_thousand_requests(cp):
+    R, D, P = 20011, 64, 16
+    g = torch.Generator().manual_seed(50)
+    lens = torch.randint(0, 3, (R,), generator=g)
+    k, v = torch.randn(2, R, 1, P, D, generator=g)
+    q = torch.randn(R, 2, D, generator=g)
+    table = torch.arange(R, dtype=torch.int32)[:, None]
+    o, lse = cp.decode(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.int().cuda(), scale=0.3)
+    pages = cp.select_pages(q.cuda(), torch.zeros(R, 1, 2, D, device="cuda"), table.cuda(), lens.int().cuda(), P, 2)
+    assert cp.sync_status() == cp.OK
+    assert torch.equal(pages.cpu()[:, 0, 0], torch.where(lens > 0, 0, -1).int()) and torch.all(pages[:, 0, 1] == -1)
+    x = 0.3 * torch.einsum("rhd,rjd->rhj", q.double(), k[:, 0, :2].double())
+    x = x.masked_fill(torch.arange(2) >= lens[:, None, None], float("-inf"))
+    want_lse = torch.logsumexp(x, -1)
+    w = torch.exp(x - want_lse.masked_fill(want_lse.isinf(), 0.0)[..., None])
+    want = torch.einsum("rhj,rjd->rhd", w, v[:, 0, :2].double())
+    assert torch.equal(lse.cpu().isneginf(), want_lse.isneginf())
+    seen = lens > 0
+    # (D + 2) 2^-24 scale sum |q k| <= 3e-5 on a score, twice that on a weight, |v| <= 6
+    assert (lse.cpu().double() - want_lse)[seen].abs().max() < 5e-5 and (o.cpu().double() - want).abs().max() < 4e-4
+    assert torch.all(o.cpu()[~seen] == 0)
+
+
 def test_decode_fp32_output_and_merge_of_two_halves_of_a_context(cp):
     """Each of two ranks holds half of the keys: their fp32 results merge to the whole."""
     c = pu.make_cache([1500, 1500], 8, 2, 128, 64, "bf16", seed=8)
@@ -306,7 +329,8 @@ def _books(R, width, num_pages, head=0, seed=0):
 
 
 @pytest.mark.parametrize("R,width,P,num_pages,most,cap", [
-    (1, 3, 16, 3, 48, 48), (5, 9, 16, 31, 90, 300), (70, 40, 32, 900, 700, 40000), (1500, 5, 64, 3500, 200, 100000)])
+    (1, 3, 16, 3, 48, 48), (5, 9, 16, 31, 90, 300), (70, 40, 32, 900, 700, 40000), (1500, 5, 64, 3500, 200, 100000),
+    (20011, 2, 16, 30000, 30, 300000)])
 def test_plan_steps_match_oracle(cp, R, width, P, num_pages, most, cap):
     g = np.random.default_rng(R)
     s = _books(R, width, num_pages, head=num_pages // 2, seed=R)
