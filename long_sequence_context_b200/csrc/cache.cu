@@ -289,7 +289,7 @@ __device__ __forceinline__ void put(CT* p, float (&f)[V], float s) {
   }
 }
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
 constexpr int kTile = 32;  // tokens whose slots one block looks at
 
 // The new rows fall into runs: tokens next to one another in one page.  A warp

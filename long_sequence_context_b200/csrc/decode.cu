@@ -267,10 +267,11 @@ struct MmaTile {
   // 8 KB of K and V at a time and twice that under way for each warp, 128 KB for an SM.
   // Measured (32768 keys x 32 heads bf16; 131072 x 8 e4m3, us): as here 84.6, 51.0; three
   // blocks of an SM 86.4, 53.0 (more partial results); three deep 87.5, 53.2; one block
-  // six deep 88.0, 65.2; e4m3 in steps of 16 keys, four deep, 54.3.
+  // six deep 88.0, 65.2; e4m3 in steps of 16 keys, four deep, 54.3.  Rows of 64 bytes (e4m3,
+  // D = 64), the most instructions for a byte, take a third block: 268 MB 51 us, else 58.
   static constexpr int kSub = 256 / kRowBytes;
   static constexpr int kDepth = 2;
-  static constexpr int kCtas = 2;
+  static constexpr int kCtas = NT == 1 && kRowBytes == 64 ? 3 : 2;
   // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
   // ends at 2^-24, which must be far below the largest weight of a long context.
   static constexpr float kLift = kHalf ? 14.f : 0.f, kSlack = kHalf ? 1.f : 8.f;
@@ -366,10 +367,7 @@ struct MmaTile {
       for (int r = 0; r < 2; ++r)
         if constexpr (kHalf) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            a[r][2 * i] = e4m3x2_to_half2((uint16_t)(w[r][2 * e + i] & 0xffffu));
-            a[r][2 * i + 1] = e4m3x2_to_half2((uint16_t)(w[r][2 * e + i] >> 16));
-          }
+          for (int i = 0; i < 2; ++i) e4m3x4_to_half(w[r][2 * e + i], a[r][2 * i], a[r][2 * i + 1]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[r][i] = w[r][4 * e + i];
@@ -441,10 +439,8 @@ struct MmaTile {
         uint32_t a0, a1, a2, a3;
         if constexpr (kHalf) {
           const int w = 2 * h + (m >> 1);
-          const uint32_t x = __byte_perm(v[0][w], v[1][w], (m & 1) ? 0x7362 : 0x5140);
-          const uint32_t y = __byte_perm(v[2][w], v[3][w], (m & 1) ? 0x7362 : 0x5140);
-          a0 = e4m3x2_to_half2((uint16_t)(x & 0xffffu)), a1 = e4m3x2_to_half2((uint16_t)(x >> 16));
-          a2 = e4m3x2_to_half2((uint16_t)(y & 0xffffu)), a3 = e4m3x2_to_half2((uint16_t)(y >> 16));
+          e4m3x4_to_half(__byte_perm(v[0][w], v[1][w], (m & 1) ? 0x7362 : 0x5140), a0, a1);
+          e4m3x4_to_half(__byte_perm(v[2][w], v[3][w], (m & 1) ? 0x7362 : 0x5140), a2, a3);
         } else {
           a0 = __byte_perm(v[0][4 * h + m], v[1][4 * h + m], 0x5410), a1 = __byte_perm(v[0][4 * h + m], v[1][4 * h + m], 0x7632);
           a2 = __byte_perm(v[2][4 * h + m], v[3][4 * h + m], 0x5410), a3 = __byte_perm(v[2][4 * h + m], v[3][4 * h + m], 0x7632);

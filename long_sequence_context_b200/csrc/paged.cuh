@@ -72,11 +72,12 @@ __device__ __forceinline__ float e4m3_scale(const float* amax) {
   return a > 0.f ? __fmul_rn(__fdiv_rn(1.f, a), 448.f) : 1.f;
 }
 
-// two e4m3 codes (low byte first) as half precision, which holds every code exactly
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t c) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
-  return r;
+// four e4m3 codes (low byte first) as two pairs in half precision, which holds every code exactly
+__device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
@@ -105,7 +106,8 @@ template <>
 struct Unpack<E4m3> {
   static constexpr int kPerWord = 4;
   __device__ static __forceinline__ void word(uint32_t w, float* f) {
-    const uint32_t a = e4m3x2_to_half2((uint16_t)(w & 0xffffu)), b = e4m3x2_to_half2((uint16_t)(w >> 16));
+    uint32_t a, b;
+    e4m3x4_to_half(w, a, b);
     const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
     const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
     f[0] = x.x;
