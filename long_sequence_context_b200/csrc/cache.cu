@@ -23,10 +23,14 @@ namespace {
 using namespace paged;
 
 constexpr int kPlanThreads = 1024;
-// One block does the whole plan up to here: a step of one token per request has
-// nothing for a second block, and a second launch costs more than the work.
-// Measured, one block against two launches (us): 16 requests 3.0, 5.0; 256 with 595
-// tokens 5.1, 6.3; 1000 with 2276 tokens 7.7, 8.0; 512 with 116,000 108, 7.0.
+// Up to kSmallR requests, each of many blocks sums them all for itself and takes its
+// share of the tokens and pages: one launch.  A block that starts late must still find
+// the lengths and the state as they were, so updating them in place takes one block up to
+// kSmallTokens tokens, and above (or with more requests) one block that sums and a second
+// launch for the rest.
+// Measured, many blocks | one block | two launches (us): 16 requests 2.9 | 2.9 | 5.0; 256
+// with 595 tokens 3.5 | 4.7 | 6.3; 1000 with 2276 4.6 | 7.7 | 8.0; 512 with 116,000
+// 5.1 | 108 | 7.4; the end of a context of 524,288 tokens 3.0 | 7.2 | -.
 constexpr int kSmallR = 1024;
 constexpr long kSmallTokens = 2048;
 
@@ -38,7 +42,7 @@ struct PlanArgs {
   int32_t *table, *ring;
   int32_t *lens_out, *state_out, *cu, *verdict;
   int64_t* slots;
-  int32_t *head, *pop_at, *push_at;  // workspace of a large plan: see Prefix
+  int32_t *head, *pop_at, *push_at;  // workspace of two launches: see Prefix
   unsigned* err;
   long long capacity;
   int R, max_pages, shift, num_pages;
@@ -48,11 +52,12 @@ struct Three {
   long long a, b, c;
 };
 
-// What the requests' prefix sums leave for the items, in shared memory (small
-// plans) or in the workspace.
+// What the requests' prefix sums leave for the items, in shared memory or in the
+// workspace (two launches).
 struct Prefix {
   int32_t *head;                     // {everything fits, the ring's head, its count}
   int32_t *cu, *pop_at, *push_at;    // [R + 1]: first new token, page taken, page returned
+  int32_t *before;                   // [R]: lengths before the step, or null: from those after it
 };
 
 __device__ __forceinline__ long long pages_of(long long n, int shift) { return (n + (1 << shift) - 1) >> shift; }
@@ -71,10 +76,10 @@ __device__ __forceinline__ Three request_of(const PlanArgs& a, int r, int* bad) 
 // Place i of the ring of n entries (i < 2 n).
 __device__ __forceinline__ int ring_at(long long i, int n) { return (int)(i >= n ? i - n : i); }
 
-// One block: prefix sums over the requests, the verdict, and everything that
-// has one value per request.  Reads all lengths before it writes any, so that
+// One block: prefix sums over the requests, the verdict, and (`writes`) everything
+// that has one value per request.  Reads all lengths before it writes any, so that
 // lens_out may be lens and state_out free_state.
-__device__ __forceinline__ void plan_requests(const PlanArgs& a, const Prefix& p) {
+__device__ __forceinline__ void plan_requests(const PlanArgs& a, const Prefix& p, bool writes) {
   __shared__ Three s_sum[32];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -124,19 +129,26 @@ __device__ __forceinline__ void plan_requests(const PlanArgs& a, const Prefix& p
     const int n = a.lens[r];
     int ignore = 0;
     const Three x = request_of(a, r, &ignore);
-    a.cu[r] = p.cu[r] = ok ? (int)at.a : 0;
+    p.cu[r] = ok ? (int)at.a : 0;
     p.pop_at[r] = ok ? (int)at.b : 0;
     p.push_at[r] = ok ? (int)at.c : 0;
-    a.lens_out[r] = ok ? n + a.delta[r] : n;
+    if (p.before) p.before[r] = n;
+    if (writes) {
+      a.cu[r] = ok ? (int)at.a : 0;
+      a.lens_out[r] = ok ? n + a.delta[r] : n;
+    }
     at.a += x.a, at.b += x.b, at.c += x.c;
   }
   if (tid == 0) {
-    a.cu[a.R] = p.cu[a.R] = ok ? (int)all.a : 0;
+    p.cu[a.R] = ok ? (int)all.a : 0;
     p.pop_at[a.R] = ok ? (int)all.b : 0;
     p.push_at[a.R] = ok ? (int)all.c : 0;
     p.head[0] = ok;
     p.head[1] = head;
     p.head[2] = count;
+  }
+  if (tid == 0 && writes) {
+    a.cu[a.R] = ok ? (int)all.a : 0;
     a.state_out[0] = ok ? ring_at(head + all.b, a.num_pages) : head;
     a.state_out[1] = ok ? (int)(count - all.b + all.c) : count;
     *a.verdict = verdict;
@@ -159,11 +171,12 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
   const bool ok = p.head[0] != 0;
   const int head = p.head[1], count = p.head[2];
   const int tokens = p.cu[a.R], pops = p.pop_at[a.R], pushes = p.push_at[a.R];
+  auto before_of = [&](int r) { return p.before ? p.before[r] : a.lens_out[r] - a.delta[r]; };  // (ok)
   for (long long i = i0; i < a.capacity; i += n) {
     long long slot = -1;
     if (i < tokens) {
       const int r = find(p.cu, a.R, (int)i);
-      const int before = a.lens_out[r] - a.delta[r];
+      const int before = before_of(r);
       const int pos = before + ((int)i - p.cu[r]);
       const int j = pos >> a.shift, held = (int)pages_of(before, a.shift);
       const int page = j < held ? a.table[(size_t)r * a.max_pages + j]
@@ -180,7 +193,7 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
   // these places is read.
   auto find_page = [&](int k, const int32_t* at, bool back, size_t& cell, int& place) {
     const int r = find(at, a.R, k);
-    const int first = (int)pages_of(back ? a.lens_out[r] : a.lens_out[r] - a.delta[r], a.shift);
+    const int first = (int)pages_of(back ? before_of(r) + a.delta[r] : before_of(r), a.shift);
     cell = (size_t)r * a.max_pages + first + (k - at[r]);
     place = ring_at((back ? ring_at((long long)head + count, a.num_pages) : head) + (long long)k, a.num_pages);
   };
@@ -215,22 +228,24 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
   move(pushes, p.push_at, true);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const PlanArgs a) {
-  __shared__ int32_t s_at[3][kSmallR + 1], s_head[3];
-  const Prefix p = {s_head, s_at[0], s_at[1], s_at[2]};
+// Every block sums the requests for itself (lens_out and state_out are other memory than
+// lens and free_state, or this is the only block) and takes its share of the items.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+  __shared__ int32_t s_at[4][kSmallR + 1], s_head[3];
+  const Prefix p = {s_head, s_at[0], s_at[1], s_at[2], s_at[3]};
   after_previous();
-  plan_requests(a, p);
+  plan_requests(a, p, blockIdx.x == 0);
   __syncthreads();
-  plan_items(a, p, threadIdx.x, blockDim.x);
+  plan_items(a, p, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
 }
 __global__ void __launch_bounds__(kPlanThreads) plan_requests_kernel(const PlanArgs a) {
   after_previous();
-  plan_requests(a, {a.head, a.cu, a.pop_at, a.push_at});
+  plan_requests(a, {a.head, a.cu, a.pop_at, a.push_at, nullptr}, true);
 }
 __global__ void __launch_bounds__(256) plan_items_kernel(const PlanArgs a) {
   __shared__ int32_t s_at[3][kSmallR + 1];
   after_previous();
-  Prefix p = {a.head, a.cu, a.pop_at, a.push_at};
+  Prefix p = {a.head, a.cu, a.pop_at, a.push_at, nullptr};
   if (a.R <= kSmallR) {  // searched in shared memory: 512 requests with 80,000 tokens 8.9 us, else 10.9
     for (int i = threadIdx.x; i <= a.R; i += blockDim.x)
       s_at[0][i] = a.cu[i], s_at[1][i] = a.pop_at[i], s_at[2][i] = a.push_at[i];
@@ -239,6 +254,8 @@ __global__ void __launch_bounds__(256) plan_items_kernel(const PlanArgs a) {
   }
   plan_items(a, p, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
 }
+
+bool overlap(const int32_t* x, const int32_t* y, long n) { return x < y + n && y < x + n; }
 
 struct AppendArgs {
   const void *k, *v;
@@ -477,23 +494,27 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   a.shift = shift;
   a.num_pages = num_pages;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!need) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const long long items = std::max<long long>(capacity, std::min<long long>((long long)R * max_pages, num_pages));
+  const unsigned blocks =
+      (unsigned)std::max<long long>(1, std::min<long long>((items + 255) / 256, (long long)num_sms(dev) * 2));
+  const bool in_place = overlap(lens, lens_out, R) || overlap(free_state, free_state_out, 2);
+  const bool many = R <= kSmallR && !in_place;
+  if (many || !need) {
+    // fewer warps' sums to add in a small block: 16 requests 3.0 us with 256 threads, 5.1 with 1024
+    const unsigned threads = many || (R <= 256 && capacity <= 1024) ? 256 : kPlanThreads;
     prof_begin(kKCachePlan, s);
-    // fewer warps' sums to add: 16 requests 3.0 us with 256 threads, 5.1 with 1024
-    const cudaError_t e = launch_chained(plan_small_kernel, dim3(1), R <= 256 && capacity <= 1024 ? 256 : kPlanThreads, 0, 0, s, a);
+    const cudaError_t e = launch_chained(plan_kernel, dim3(many ? blocks : 1), threads, 0, 0, s, a);
     prof_end(kKCachePlan, s);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CPATTN_ERR_CUDA;
     add_launches(1);
     return CPATTN_OK;
   }
-  int dev = 0;
-  cudaGetDevice(&dev);
   prof_begin(kKCachePlan, s);
   cudaError_t e = launch_chained(plan_requests_kernel, dim3(1), kPlanThreads, 0, 0, s, a);
   prof_end(kKCachePlan, s);
   if (e != cudaSuccess) return CPATTN_ERR_CUDA;
-  const long long items = std::max<long long>(capacity, std::min<long long>((long long)R * max_pages, num_pages));
-  const unsigned blocks = (unsigned)std::max<long long>(1, std::min<long long>((items + 255) / 256, (long long)num_sms(dev) * 8));
   prof_begin(kKCachePlan, s);
   e = launch_chained(plan_items_kernel, dim3(blocks), 256, 0, 0, s, a);
   prof_end(kKCachePlan, s);

@@ -385,6 +385,33 @@ def test_plan_in_place_and_again(cp):
     assert torch.equal(got[3], once[3])
 
 
+@pytest.mark.parametrize("which", ["lens", "state", "both"])
+@pytest.mark.parametrize("R,cap", [(7, 600), (1000, 2048), (7, 2049), (1024, 70000), (1025, 70000)])
+def test_plan_in_place_matches_oracle(cp, R, cap, which):
+    """Lengths, state or both updated where they are, at sizes on both sides of every limit of the launches."""
+    P, width = 16, 8
+    g = np.random.default_rng(R + cap)
+    s = _books(R, width, R * width, head=R, seed=cap)
+    most = min(60, cap // R)
+    for step in range(4):
+        lens = s["lens"].tolist()
+        delta = [-n if g.integers(5) == 0 else int(g.integers(-min(n, 40), min(most, width * P - n) + 1)) for n in lens]
+        want = paged.plan(lens, delta, s["table"].cpu().numpy(), s["ring"].tolist(), s["state"].tolist(), P, cap)
+        kw = {}
+        if which != "state":
+            kw["lens_out"] = s["lens"]
+        if which != "lens":
+            kw["free_state_out"] = s["state"]
+        out = cp.cache_plan(s["lens"], torch.tensor(delta, dtype=torch.int32, device="cuda"), s["table"], s["ring"],
+                            s["state"], P, cap, **kw)
+        assert out[4].item() == want[6] == 0
+        s["lens"], s["state"] = out[0], out[1]
+        assert out[0].tolist() == want[0] and out[1].tolist() == want[3]
+        assert out[2].tolist() == want[4] and out[3].tolist() == want[5]
+        assert np.array_equal(s["table"].cpu().numpy(), want[1]) and s["ring"].tolist() == want[2]
+        assert cp.sync_status() == cp.OK
+
+
 # ---- rows ----
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3"])
