@@ -435,6 +435,8 @@ int cpattn_select_pages(const void* q, const void* k_bounds, const int32_t* bloc
  * over the lens[r] tokens of request r (the new token's own among them once it is
  * appended), or over those in the listed pages.  Query head i reads kv head
  * i / (Hq / Hkv).
+ *   block_table    [R][max_pages]; short contexts are answered faster in a table
+ *                  that is not much wider than they need
  *   q              [R][Hq][D] dtype
  *   pages          NULL, or [R][Hkv][budget] int32 as cpattn_select_pages writes it:
  *                  the first min(budget, held pages) entries are read, negative

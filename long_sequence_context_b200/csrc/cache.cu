@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   const bool first = mine >= 0 && !bad && ((mine & page_mask) == 0 || before != mine - 1);
   const uint32_t runs = __ballot_sync(0xffffffffu, first);
   const int nth = __popc(runs & ((1u << lane) - 1u));
-  const float ks = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax) : 1.f;
-  const float vs = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax + 1) : 1.f;
+  const float ks = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax[0]) : 1.f;
+  const float vs = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax[1]) : 1.f;
   const int sub = lane / kLanes, d = lane % kLanes * V;
 
   const int items = __popc(runs) * a.Hkv;

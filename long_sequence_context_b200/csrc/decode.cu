@@ -12,14 +12,20 @@
 // partial result (running maximum, sum, unnormalised output, all fp32) per block,
 // and join_kernel combines them by the log-sum-exp rule of cpattn_merge.
 //
+// Where the table (or the selection) has room for a few units a block only, a cluster
+// of up to 16 blocks takes each pair instead and joins through shared memory: one
+// launch, and no search for a share (see one_cluster).
+//
 // What bounds it: K and V are read once, in bf16 and for up to 16 heads a group at
 // 93 to 99% of a plain copy's bandwidth (32768 keys x 32 heads x 128: 537 MB in 84
 // us, 6.4 TB/s; 131072 x 8 heads in e4m3, where the codes' widening doubles the
-// instructions for a byte: 268 MB in 51 us), beside some 6 us of start, partial
-// results and join, which is what short contexts take.  Groups of 32 heads wait for
-// their instructions (268 MB in 70 us); sharing a ring between the warps of a group
-// took longer (77), and so did fewer blocks with more units each (257 keys x 16
-// heads: one unit a block 6.9 us, two 7.3, four 8.6).
+// instructions for a byte: 268 MB in 49 us), beside some 6 us of start, partial
+// results and join.  Short contexts wait for a chain of latencies (launch, length,
+// page, keys, join): 16 keys take 4.5 to 6 us, 257 keys x 16 heads 5.2.  Groups of 32
+// heads wait for their instructions (268 MB in 70 us); sharing a ring between the warps
+// of a group took longer (77).
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "cpattn.h"
@@ -32,6 +38,7 @@ namespace cpattn {
 namespace {
 
 using namespace paged;
+namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -142,6 +149,7 @@ struct FmaTile {
   // thread blocks of an SM.  Many warps hide the arithmetic better than deep rings (268 MB,
   // D = 128: as here 55 us; two blocks one deep 59, one block two deep 62).
   static constexpr int kSub = 1, kDepth = D == 128 ? 1 : 2, kCtas = NT == 1 ? 3 : 2;
+  static constexpr int kOneUnits = 3;    // of a block, at most, where a cluster takes a pair
   static constexpr int kLines = D / 32;  // of a row
 
   __device__ static __forceinline__ int col(int h, int g, int e) { return 64 * h + 8 * g + e; }
@@ -266,12 +274,12 @@ struct MmaTile {
   static constexpr int kQueryBytes = D * 2;
   static constexpr int kRowBytes = D * (int)sizeof(C);  // 256, 128 or 64
   // 8 KB of K and V at a time and twice that under way for each warp, 128 KB for an SM.
-  // Measured (32768 keys x 32 heads bf16; 131072 x 8 e4m3, us): as here 84.6, 51.0; three
+  // Measured (32768 keys x 32 heads bf16; 131072 x 8 e4m3, us): as here 84.6, 51.0 then; three
   // blocks of an SM 86.4, 53.0 (more partial results); three deep 87.5, 53.2; one block
   // six deep 88.0, 65.2; e4m3 in steps of 16 keys, four deep, 54.3.  Rows of 64 bytes (e4m3,
   // D = 64), the most instructions for a byte, take a third block: 268 MB 51 us, else 58.
   static constexpr int kSub = 256 / kRowBytes;
-  static constexpr int kDepth = 2;
+  static constexpr int kDepth = 2, kOneUnits = 4;
   static constexpr int kCtas = NT == 1 && kRowBytes == 64 ? 3 : 2;
   // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
   // ends at 2^-24, which must be far below the largest weight of a long context.
@@ -319,15 +327,18 @@ struct MmaTile {
         const unsigned quad = 0xfu << (threadIdx.x & 28);
         m = fmaxf(m, __shfl_xor_sync(quad, m, 1));
         m = fmaxf(m, __shfl_xor_sync(quad, m, 2));
-        // 2^up m in [2^14, 2^15)
-        const int up = m > 0.f && m < INFINITY ? 14 - ilogbf(m) : 0;
-        if (t == 0) unit[head] = ldexpf(1.f, -up);
+        // 2^up m in [2^14, 2^15), below it if m is subnormal; by two factors, since 2^up may
+        // be no fp32 number (what the first one rounds ends as zero)
+        const int up = m > 0.f && m < INFINITY ? 14 + 127 - (int)(__float_as_uint(m) >> 23) : 0;
+        auto power = [](int n) { return __int_as_float((127 + n) << 23); };
+        const float up0 = power(up / 2), up1 = power(up - up / 2);
+        if (t == 0) unit[head] = power(-(up / 2)) * power(up / 2 - up);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
           uint32_t u[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const __half2 x = __floats2half2_rn(ldexpf(f[e][2 * i], up), ldexpf(f[e][2 * i + 1], up));
+            const __half2 x = __floats2half2_rn(f[e][2 * i] * up0 * up1, f[e][2 * i + 1] * up0 * up1);
             u[i] = *reinterpret_cast<const uint32_t*>(&x);
           }
           w[e] = make_uint4(u[0], u[1], u[2], u[3]);
@@ -455,7 +466,8 @@ struct MmaTile {
   }
 };
 
-template <typename Tile, int D, int NT>
+// ONE: a cluster of thread blocks takes one (request, kv head); else the line.
+template <typename Tile, int D, int NT, bool ONE>
 __global__ void __launch_bounds__(kThreads, Tile::kCtas)
     decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using CT = typename Tile::CT;
@@ -477,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
   __shared__ float s_m[kWarps][HT], s_l[kWarps][HT];
   __shared__ int s_scan[kWarps], s_base;
   __shared__ int s_r;
+  __shared__ float2 s_ml[ONE ? kGroups * HT : 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x;
@@ -490,80 +503,99 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
   }
   after_previous();
 
-  // requests without a key: o = 0, lse = -inf
-  for (int r = cta; r < a.R; r += gridDim.x) {
-    if (request_units<UNIT>(a, request_len(a, r, tid == 0)) != 0) continue;
-    if (a.by_pair)
-      for (int h = tid; h < a.Hkv; h += kThreads) a.tail[r * a.Hkv + h] = make_int4(-1, 0, 0, 0);
-    const float none[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 4 * tid; i < a.Hq * D; i += 4 * kThreads) store_o<4>(a, (size_t)r * a.Hq * D + i, none);
-    for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)r * a.Hq + i] = -INFINITY;
-  }
-
-  // this block's share of the line
-  auto weight = [&](int r) { return pair_weight(request_units<UNIT>(a, request_len(a, r, false))) * a.Hkv; };
-  const int per = (a.R + kThreads - 1) / kThreads;
-  const int r_lo = min(tid * per, a.R), r_hi = min(r_lo + per, a.R);
-  int mine = 0;
-  for (int r = r_lo; r < r_hi; ++r) mine += weight(r);
-  int upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
-  if (lane == 31) s_scan[warp] = upto;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += s_scan[w];
-    total += s_scan[w];
-  }
-  // `each` units for every block and one more for the first `more`
-  const int n_cta = max(1, min((int)gridDim.x, total)), each = total / n_cta, more = total - each * n_cta;
-  int u = each * cta + min(cta, more);
-  const int u_end = cta < n_cta ? u + each + (cta < more ? 1 : 0) : u;
-  if (u >= u_end) {
-    if (tid == 0 && !a.by_pair) a.tail[cta] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-  if (upto - mine <= u && u < upto) {  // one thread's requests hold the first unit
-    int base = upto - mine, r = r_lo;
-    for (; r < r_hi - 1; ++r) {
-      const int n = weight(r);
-      if (u < base + n) break;
-      base += n;
+  int u = 0, u_end = 0, r = 0, base = 0, each = 0, more = 0;
+  if constexpr (!ONE) {
+    // requests without a key: o = 0, lse = -inf
+    for (int r = cta; r < a.R; r += gridDim.x) {
+      if (request_units<UNIT>(a, request_len(a, r, tid == 0)) != 0) continue;
+      if (a.by_pair)
+        for (int h = tid; h < a.Hkv; h += kThreads) a.tail[r * a.Hkv + h] = make_int4(-1, 0, 0, 0);
+      const float none[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = 4 * tid; i < a.Hq * D; i += 4 * kThreads) store_o<4>(a, (size_t)r * a.Hq * D + i, none);
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)r * a.Hq + i] = -INFINITY;
     }
-    s_r = r;
-    s_base = base;
+
+    // this block's share of the line
+    auto weight = [&](int r) { return pair_weight(request_units<UNIT>(a, request_len(a, r, false))) * a.Hkv; };
+    const int per = (a.R + kThreads - 1) / kThreads;
+    const int r_lo = min(tid * per, a.R), r_hi = min(r_lo + per, a.R);
+    int mine = 0;
+    for (int r = r_lo; r < r_hi; ++r) mine += weight(r);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += s_scan[w];
+      total += s_scan[w];
+    }
+    // `each` units for every block and one more for the first `more`
+    const int n_cta = max(1, min((int)gridDim.x, total));
+    each = total / n_cta, more = total - each * n_cta;
+    u = each * cta + min(cta, more);
+    u_end = cta < n_cta ? u + each + (cta < more ? 1 : 0) : u;
+    if (u >= u_end) {
+      if (tid == 0 && !a.by_pair) a.tail[cta] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    if (upto - mine <= u && u < upto) {  // one thread's requests hold the first unit
+      int base = upto - mine, r = r_lo;
+      for (; r < r_hi - 1; ++r) {
+        const int n = weight(r);
+        if (u < base + n) break;
+        base += n;
+      }
+      s_r = r;
+      s_base = base;
+    }
+    __syncthreads();
+    r = s_r, base = s_base;
   }
-  __syncthreads();
-  int r = s_r, base = s_base;
 
   const int hgroups = a.group <= HT ? 1 : (a.group <= 2 * HT ? 2 : 4);  // head groups: warps share keys
   const int kwarps = kWarps / hgroups;
   const int hg = warp % hgroups, kw = warp / hgroups;
-  const float scale_log2 =
-      sizeof(CT) == 1 ? a.scale_log2 / e4m3_scale(a.kv_amax) : a.scale_log2;
-  const float v_unit = sizeof(CT) == 1 ? __fdiv_rn(1.f, e4m3_scale(a.kv_amax + 1)) : 1.f;
+  float amax[2] = {0.f, 0.f};  // asked for here, looked at when the first keys are under way
+  if constexpr (sizeof(CT) == 1) {
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(amax[0]) : "l"(a.kv_amax));
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(amax[1]) : "l"(a.kv_amax + 1));
+  }
   int4 tail = make_int4(-1, 0, 0, 0);
   unsigned issued = 0, done = 0;  // blocks this warp has asked for and used
 
-  while (u < u_end) {
-    const int len = request_len(a, r, false);
-    const int n_units = request_units<UNIT>(a, len), w_pair = pair_weight(n_units);
-    if (u >= base + w_pair * a.Hkv) {
-      base += w_pair * a.Hkv;
-      if (++r >= a.R) break;  // not with lengths that stand still
-      continue;
+  const int ranks = ONE ? (int)cg::this_cluster().num_blocks() : 1;
+  const int rank = ONE ? (int)cg::this_cluster().block_rank() : 0;
+  for (bool once = true; ONE ? once : u < u_end; once = false) {
+    int len, n_units, w_pair = 0, h, x0, x1;
+    if constexpr (ONE) {
+      const int pair = cta / ranks;
+      r = pair / a.Hkv, h = pair - r * a.Hkv;
+      len = request_len(a, r, tid == 0 && rank == 0);
+      n_units = request_units<UNIT>(a, len);
+      // A block without units goes on: all of the cluster meet at its barriers.
+      x0 = (int)((long long)n_units * rank / ranks), x1 = (int)((long long)n_units * (rank + 1) / ranks);
+    } else {
+      len = request_len(a, r, false);
+      n_units = request_units<UNIT>(a, len), w_pair = pair_weight(n_units);
+      if (u >= base + w_pair * a.Hkv) {
+        base += w_pair * a.Hkv;
+        if (++r >= a.R) break;  // not with lengths that stand still
+        continue;
+      }
+      h = (u - base) / w_pair;
+      const int y0 = u - base - h * w_pair;
+      const int y1 = min(w_pair, y0 + (u_end - u));
+      u += y1 - y0;
+      // the pair's own cost stands before its units
+      x0 = max(0, y0 - kPairCost), x1 = max(0, y1 - kPairCost);
+      if (x0 == x1) continue;
     }
-    const int h = (u - base) / w_pair, y0 = u - base - h * w_pair;
-    const int y1 = min(w_pair, y0 + (u_end - u));
-    u += y1 - y0;
-    // the pair's own cost stands before its units
-    const int x0 = max(0, y0 - kPairCost), x1 = max(0, y1 - kPairCost);
-    if (x0 == x1) continue;
     const int n_list = listed_pages(a, len), held = (int)(((unsigned)len + (1u << a.shift) - 1u) >> a.shift);
     const int32_t* table = a.table + (size_t)r * a.max_pages;
     const int32_t* list = a.pages ? a.pages + ((size_t)r * a.Hkv + h) * a.budget : nullptr;
@@ -604,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
         s_valid[warp][slot][sub] = valid;
         if (valid > 0 && !s_abort) {
           sm100::mbar_expect_tx(&s_full[warp][slot], 2 * kBlock);
-          if (!(a.stall && base + h + x0 + warp + i == 0))  // else: failure-detection tests only
+          if (!(a.stall && base + r + h + x0 + warp + i == 0))  // else: failure-detection tests only
             sm100::tma_load_2d(to, &k_map, &s_full[warp][slot], 0, line);
           sm100::tma_load_2d(to + kBlock, &v_map, &s_full[warp][slot], 0, line);
         } else {
@@ -634,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
         for (int e = 0; e < 16; ++e) acc[nt][hh][e] = 0.f;
     }
 
+    const float scale_log2 = sizeof(CT) == 1 ? a.scale_log2 / e4m3_scale(amax[0]) : a.scale_log2;
     const char* s_q = s_queries + hg * HT * Tile::kQueryBytes;
     float unit[NT][2];
 #pragma unroll
@@ -736,6 +769,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
                 make_float4(acc[nt][hh][2 * e + i], acc[nt][hh][2 * e + 2 + i], acc[nt][hh][2 * e + 4 + i], acc[nt][hh][2 * e + 6 + i]);
       }
     __syncthreads();
+    const float v_unit = sizeof(CT) == 1 ? __fdiv_rn(1.f, e4m3_scale(amax[1])) : 1.f;
     const bool whole = x0 == 0 && x1 == n_units;
     const int slot = 2 * cta + (x0 == 0 ? 1 : 0);
     for (int i = tid; i < a.group * (D / 4); i += kThreads) {
@@ -750,7 +784,10 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) oo[e] *= v_unit;
-      if (whole) {
+      if constexpr (ONE) {  // in place: no other thread reads these four
+        *reinterpret_cast<float4*>(&s_buf[hw * HT + hh][d]) = make_float4(oo[0], oo[1], oo[2], oo[3]);
+        if (d == 0) s_ml[head] = make_float2(mm, ll);
+      } else if (whole) {
         finish<4>(a, (size_t)r * a.Hq + (size_t)h * a.group + head, D, d, oo, mm, ll);
       } else {
         const size_t at = (size_t)slot * a.group + head;
@@ -758,7 +795,30 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
         if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mm, ll);
       }
     }
-    if (x0 == 0) {
+    if constexpr (ONE) {
+      // every block joins a share of the outputs
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      const int n = a.group * (D / 4), share = (n + ranks - 1) / ranks;
+      for (int i = rank * share + tid; i < min(n, (rank + 1) * share); i += kThreads) {
+        const int head = i / (D / 4), d = i % (D / 4) * 4;
+        float2* ml = &s_ml[head];
+        float4* from = reinterpret_cast<float4*>(&s_buf[head / HT * HT + head % HT][d]);
+        float mm = kNothing, ll = 0.f, oo[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int c = 0; c < ranks; ++c) mm = fmaxf(mm, cluster.map_shared_rank(ml, c)->x);
+#pragma unroll 8
+        for (int c = 0; c < ranks; ++c) {
+          const float2 p = *cluster.map_shared_rank(ml, c);
+          const float4 x = *cluster.map_shared_rank(from, c);
+          const float f = exp2_fast(p.x - mm);
+          ll = fmaf(f, p.y, ll);
+          oo[0] = fmaf(f, x.x, oo[0]), oo[1] = fmaf(f, x.y, oo[1]), oo[2] = fmaf(f, x.z, oo[2]), oo[3] = fmaf(f, x.w, oo[3]);
+        }
+        finish<4>(a, (size_t)r * a.Hq + (size_t)h * a.group + head, D, d, oo, mm, ll);
+      }
+      cluster.sync();  // no block leaves while its results are read
+    } else if (x0 == 0) {
       if (!whole) {  // the block that holds the pair's last unit
         const int last = base + (h + 1) * w_pair - 1, long_ones = more * (each + 1);
         tail = make_int4(r, h, last < long_ones ? last / (each + 1) : more + (last - long_ones) / each, cta);
@@ -766,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
       if (tid == 0 && a.by_pair) a.tail[r * a.Hkv + h] = whole ? make_int4(-1, 0, 0, 0) : tail;
     }
   }
-  if (tid == 0 && !a.by_pair) a.tail[cta] = tail;
+  if (!ONE && tid == 0 && !a.by_pair) a.tail[cta] = tail;
 }
 
 // Combines the partial results of a pair that starts in one block and continues
@@ -857,23 +917,59 @@ size_t ws_part_o(int grid, int group, int D) { return (size_t)2 * grid * group *
 size_t ws_part_ml(int grid, int group) { return ((size_t)2 * grid * group * 2 * sizeof(float) + 15) & ~(size_t)15; }
 constexpr int kMostCtas = 3;  // blocks of an SM, over all variants
 
+// Blocks of the cluster that takes each of `pairs` pairs of up to `units` units, when all
+// of them fit on the GPU at once (`places`) and no block has more than `most` units: 0 if not.
+// With more units a block its ring idles at the start and end of a pair, and pairs of
+// different lengths end at different times, which the line levels.  Measured, clusters |
+// line (us): bf16, 8 heads, 257 keys 5.2 | 6.7, 1024 6.2 | 7.5, 4096 (four units a block)
+// 8.7 | 9.0; 32 requests x 4 heads of 257 keys 8.7 | 10.4; fp32, 8 heads, 1024 keys 6.5 |
+// 8.1, four units a block 12.4 | 11.0.  Clusters of up to 8 blocks: 2048 keys 7.6 and with
+// 16 6.5 (2 heads).
+constexpr unsigned kMostCluster = 16;
+unsigned one_cluster(long long pairs, long long units, long long places, int most) {
+  unsigned cluster = 1;
+  while (cluster < kMostCluster && cluster < units && pairs * cluster * 2 <= places) cluster *= 2;
+  return pairs * cluster <= places && units <= (long long)most * cluster ? cluster : 0;
+}
+
+
 template <typename Tile, int D, int NT>
 int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
   static_assert(Tile::kCtas <= kMostCtas, "the workspace is sized for kMostCtas");
+  CUtensorMap k_map, v_map;
+  constexpr int kBlock = kChunk * D * (int)sizeof(typename Tile::CT), kUnit = kWarps * Tile::kSub * kChunk;
+  constexpr int kBytes = kWarps * Tile::kDepth * Tile::kSub * 2 * kBlock + 1024;
+  const uint64_t lines = ((uint64_t)a.num_pages * a.Hkv << a.shift) * (kBlock / kChunk) / 128;
+  if (!make_tmap_u8_2d(&k_map, a.k, lines, 128, 128, kBlock / 128) || !make_tmap_u8_2d(&v_map, a.v, lines, 128, 128, kBlock / 128))
+    return -1;
+  cudaError_t e;
+  const long long pairs = (long long)a.R * a.Hkv, places = decode_grid(Tile::kCtas, 1LL << 40);
+  const long long listed = a.pages ? std::min(a.budget, a.max_pages) : a.max_pages;
+  const long long pair_units = ((listed << a.shift) + kUnit - 1) / kUnit;
+  const unsigned cluster = one_cluster(pairs, pair_units, places, Tile::kOneUnits);
+  if (cluster) {
+    static std::atomic<unsigned long long> done{0};
+    auto* kernel = decode_kernel<Tile, D, NT, true>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+    if (!(done.load() & (1ull << dev)) &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return -1;
+    if (!smem_attr_once(kernel, kBytes, done)) return -1;
+    prof_begin(kKDecode, s);
+    e = launch_chained(kernel, dim3((unsigned)pairs * cluster), kThreads, kBytes, cluster, s, a, k_map, v_map);
+    prof_end(kKDecode, s);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
+  }
+  static std::atomic<unsigned long long> done{0};
+  if (!smem_attr_once(decode_kernel<Tile, D, NT, false>, kBytes, done)) return -1;
   const int grid = decode_grid(Tile::kCtas, max_units);
-  a.by_pair = (long long)a.R * a.Hkv < grid;
+  a.by_pair = pairs < grid;
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float*>(ws + ws_part_o(grid, a.group, D));
   a.tail = reinterpret_cast<int4*>(ws + ws_part_o(grid, a.group, D) + ws_part_ml(grid, a.group));
-  CUtensorMap k_map, v_map;
-  constexpr int kBlock = kChunk * D * (int)sizeof(typename Tile::CT), kBytes = kWarps * Tile::kDepth * Tile::kSub * 2 * kBlock + 1024;
-  const uint64_t lines = ((uint64_t)a.num_pages * a.Hkv << a.shift) * (kBlock / kChunk) / 128;
-  static std::atomic<unsigned long long> done{0};
-  if (!make_tmap_u8_2d(&k_map, a.k, lines, 128, 128, kBlock / 128) || !make_tmap_u8_2d(&v_map, a.v, lines, 128, 128, kBlock / 128) ||
-      !smem_attr_once(decode_kernel<Tile, D, NT>, kBytes, done))
-    return -1;
   prof_begin(kKDecode, s);
-  cudaError_t e = launch_chained(decode_kernel<Tile, D, NT>, dim3(grid), kThreads, kBytes, 0, s, a, k_map, v_map);
+  e = launch_chained(decode_kernel<Tile, D, NT, false>, dim3(grid), kThreads, kBytes, 0, s, a, k_map, v_map);
   prof_end(kKDecode, s);
   if (e != cudaSuccess) return -1;
   // Few pairs can have many parts: a large block for each head.  Else blocks of

@@ -67,9 +67,8 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned threads, si
 // tensor in PyTorch, so that codes a program writes with torch and codes written
 // here agree bit for bit.  (The one-step quotient of cpattn_quantize_e4m3 can
 // differ in the last bit.)
-__device__ __forceinline__ float e4m3_scale(const float* amax) {
-  const float a = *amax;
-  return a > 0.f ? __fmul_rn(__fdiv_rn(1.f, a), 448.f) : 1.f;
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  return amax > 0.f ? __fmul_rn(__fdiv_rn(1.f, amax), 448.f) : 1.f;
 }
 
 // four e4m3 codes (low byte first) as two pairs in half precision, which holds every code exactly

@@ -86,6 +86,44 @@ def test_decode_large_scores(cp, kind):
     pu.assert_decode(o, lse, ref, 128, 8.0, 777, kind)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,P", [
+    ([1], 1, 1, 64, 16),
+    ([0, 5, 0], 4, 2, 64, 32),
+    ([257], 16, 16, 128, 16),
+    ([700, 0, 64, 333], 12, 4, 64, 16),
+    ([513, 130], 9, 1, 128, 64),
+    ([1024, 1023, 1, 512], 34, 2, 64, 32),
+    ([2048, 77], 48, 1, 128, 256),
+    ([0, 0], 128, 2, 64, 16),
+    ([128] * 37, 8, 4, 128, 16),
+    ([0, 300, 50, 129] * 10, 5, 5, 64, 64),
+    ([4096], 24, 8, 64, 128),
+])
+def test_decode_with_a_table_just_wide_enough_and_with_a_wide_one(cp, kind, lens, Hq, Hkv, D, P):
+    """The table's width decides how the keys are dealt to blocks: both ways, all cluster sizes."""
+    refs = []
+    for width in (max(1, -(-max(lens) // P)), 8192 // P, 65536 // P):
+        c = pu.make_cache(lens, Hq, Hkv, D, P, kind, seed=sum(lens) + Hq, width=width)
+        refs = refs or [pu.reference(c, D ** -0.5)]
+        for out_dtype in (None, torch.float32):
+            o, lse = _decode(cp, c, D ** -0.5, out_dtype=out_dtype)
+            pu.assert_decode(o, lse, refs[0], D, D ** -0.5, max(lens), kind, str(width))
+
+
+@pytest.mark.parametrize("kind,exponent", [(k, e) for k in ("bf16", "fp32", "e4m3") for e in (-100, -60, 60, 100)] +
+                         [("e4m3", -133), ("e4m3", -128), ("e4m3", -126)])
+def test_decode_queries_of_any_size(cp, kind, exponent):
+    """A scale that brings the scores back to ordinary ones, as far as it goes; 8-bit keys
+    take queries down to the subnormal ones, which they scale into half precision."""
+    c = pu.make_cache([300, 40], 6, 2, 128, 32, kind, seed=14)
+    c["q"] = (c["q"].double() * 2.0 ** exponent).to(c["q"].dtype)
+    scale = 2.0 ** max(-124, min(124, -exponent)) * 128 ** -0.5
+    ref = pu.reference(c, scale)
+    o, lse = _decode(cp, c, scale)
+    pu.assert_decode(o, lse, ref, 128, scale, 300, kind)
+
+
 def test_a_batch_of_twenty_thousand_requests(cp):
     R, D, P = 20011, 64, 16
     g = torch.Generator().manual_seed(50)
@@ -642,6 +680,34 @@ def test_decode_wait_that_runs_out_is_reported_and_the_device_stays_usable(cp, h
     assert st == cp.ERR_TIMEOUT, cp.status_str(st)
     o, lse = _decode(cp, c, 0.125)
     pu.assert_decode(o, lse, pu.reference(c, 0.125), 64, 0.125, 900, "bf16", "after it")
+
+
+@pytest.mark.parametrize("kind,group", [("bf16", 2), ("e4m3", 20), ("fp32", 2)])
+def test_decode_wait_that_runs_out_in_a_wide_table(cp, kind, group):
+    c = pu.make_cache([900, 70], 2 * group, 2, 64, 32, kind, seed=45, width=2000)
+    assert cp.sync_status() == cp.OK
+    cp.debug_stall(1)
+    try:
+        d = pu.on_gpu(c)
+        cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], kv_amax=d["amax"])
+        st = cp.sync_status()
+    finally:
+        cp.debug_stall(0)
+    assert st == cp.ERR_TIMEOUT, cp.status_str(st)
+    o, lse = _decode(cp, c, 0.125)
+    pu.assert_decode(o, lse, pu.reference(c, 0.125), 64, 0.125, 900, kind, "after it")
+
+
+@pytest.mark.parametrize("width", [8, 4000])
+def test_decode_bad_pages_in_narrow_and_wide_tables(cp, width):
+    c = pu.make_cache([100, 64], 2, 1, 64, 16, "bf16", seed=46, width=width)
+    d = pu.on_gpu(c)
+    bad = d["table"].clone()
+    bad[0, 1], bad[1, 3] = c["k"].shape[0], -1
+    o, lse = cp.decode(d["q"], d["k"], d["v"], bad, d["lens"], scale=0.1)
+    assert cp.sync_status() == cp.ERR_PAGE and cp.sync_status() == cp.OK
+    keep = [[[0, 2, 3, 4, 5, 6]], [[0, 1, 2]]]
+    pu.assert_decode(o, lse, pu.reference(c, 0.1, keep), 64, 0.1, 100, "bf16")
 
 
 def test_select_with_operands_below_the_normal_range(cp):
