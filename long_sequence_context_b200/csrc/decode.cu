@@ -274,7 +274,7 @@ struct MmaTile {
   static constexpr int kQueryBytes = D * 2;
   static constexpr int kRowBytes = D * (int)sizeof(C);  // 256, 128 or 64
   // 8 KB of K and V at a time and twice that under way for each warp, 128 KB for an SM.
-  // Measured (32768 keys x 32 heads bf16; 131072 x 8 e4m3, us): as here 84.6, 51.0 then; three
+  // Measured (32768 keys x 32 heads bf16; 131072 x 8 e4m3, us): as here 84.6, 51.0 (e4m3 has gained 2 since); three
   // blocks of an SM 86.4, 53.0 (more partial results); three deep 87.5, 53.2; one block
   // six deep 88.0, 65.2; e4m3 in steps of 16 keys, four deep, 54.3.  Rows of 64 bytes (e4m3,
   // D = 64), the most instructions for a byte, take a third block: 268 MB 51 us, else 58.

@@ -318,8 +318,8 @@ struct Approx {
     return fmaxf(__low2float(most), __high2float(most));
   }
 
-  // The score of one page in 64 bits, by a whole warp.
-  __device__ static uint32_t rescore(const SelectArgs& a, const Pair& p, int j) {
+  // The largest score of page j over heads h0 .. h1 - 1 in 64 bits, by a whole warp.
+  __device__ static uint32_t rescore(const SelectArgs& a, const Pair& p, int j, int h0, int h1) {
     const int lane = threadIdx.x & 31;
     constexpr int V = D / 32;  // columns of a lane
     const int page = p.table[j];
@@ -341,7 +341,7 @@ struct Approx {
     }
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)p.r * a.Hq + (size_t)p.h * a.group) * D + lane * V;
     uint32_t key = 0u;
-    for (int m = 0; m < a.group; ++m) {
+    for (int m = h0; m < h1; ++m) {
       double sum = 0.;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -473,8 +473,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   Scores scores;
   Pair p = {pair / a.Hkv, pair % a.Hkv, 0, 0, nullptr};
 
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block has started
+  if (tid == 0) s_listed = 0u;
   after_previous();
   scores.queries(a, p.r, p.h, 0);
+  p.table = a.table + (size_t)p.r * a.max_pages;
+  for (int i = 32 * (rank * kThreads + tid); i < a.max_pages; i += 32 * kThreads * ranks)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + i));  // while the length is under way
   const long long cap = (long long)a.max_pages << a.shift;
   long long len = a.lens[p.r];
   if (len < 0 || len > cap) {
@@ -484,15 +489,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   const int held = (int)((len + (1 << a.shift) - 1) >> a.shift);
   if (held <= a.budget) {  // everything is selected (the whole cluster leaves here)
     for (int j = rank * kThreads + tid; j < a.budget; j += ranks * kThreads) out[j] = j < held ? j : -1;
+    cluster.barrier_wait();
     return;
   }
-  if (tid == 0) s_listed = 0u;
-  cluster.barrier_arrive();  // no block writes to the first one before that has started
 
   const int per = (held + ranks - 1) / ranks;
   p.first = min(rank * per, held);
   p.n = min(per, held - p.first);
-  p.table = a.table + (size_t)p.r * a.max_pages;
   uint32_t* keys = cluster.map_shared_rank(s_key, 0);
   for (int h0 = 0; h0 < a.group; h0 += 8) {
     if (h0 > 0) {
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     }
     scores.begin(a, p);
     scores.stage(a, p, h0, s_q, s_norm);
-    if (h0 == 0) cluster.barrier_wait();
+    if (h0 == 0) cluster.barrier_wait();  // no block writes to the first one before that has started
     __syncthreads();
     float most = scores.score(a, p, h0, s_q, [&](int j, uint32_t key) {
       if (j < a.keep_first || j == held - 1) key = kAlways;
@@ -528,9 +531,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   uint32_t threshold;
   int need;
   find_threshold(s_key, held, a.budget, kApprox, s_search, threshold, need);
-  // a stretch of pages for each warp, in steps of 32
-  const int stretch = ((held + kWarps - 1) / kWarps + 31) & ~31;
-  const int w0 = min(warp * stretch, held), w1 = min(w0 + stretch, held);
+  // a stretch of pages for each thread
+  const int mine = 4 * ((held + 4 * kThreads - 1) / (4 * kThreads));
+  const int i0 = min(tid * mine, held), i1 = min(i0 + mine, held);
+  auto each = [&](auto f) {
+    for (int i = i0; i < i1; i += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
+      f(i, k.x);
+      if (i + 1 < i1) f(i + 1, k.y);
+      if (i + 2 < i1) f(i + 2, k.z);
+      if (i + 3 < i1) f(i + 3, k.w);
+    }
+  };
   if constexpr (kApprox) {
     if (threshold != kAlways - 1u) {
       // [low, high]: the keys within 2 eps of the threshold
@@ -545,34 +557,33 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       uint32_t low = 0u, high = kAlways - 1u;
       if (threshold != 0u && eps < 1e37f && fabsf(at) < 1e37f)
         low = order_key(__fadd_rd(at, -2.f * eps)), high = min(high, order_key(__fadd_ru(at, 2.f * eps)));
-      uint32_t above = 0, within = 0;
-      for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t key = s_key[i];
+      uint32_t above = 0;
+      each([&](int i, uint32_t key) {
         above += key > high;
-        within += key >= low && key <= high;
-      }
+        if (key >= low && key <= high) {
+          const uint32_t at = atomicAdd(&s_listed, 1u);
+          if (at < (uint32_t)kThreads) s_list[at] = i, s_search.bin[at] = 0u;
+        }
+      });
       above = __reduce_add_sync(0xffffffffu, above);
-      within = __reduce_add_sync(0xffffffffu, within);
-      if (lane == 0) s_count[0][warp] = above, s_count[1][warp] = within;
+      if (lane == 0) s_count[0][warp] = above;
       __syncthreads();
-      above = within = 0;
+      const uint32_t within = s_listed;
+      above = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) above += s_count[0][w], within += s_count[1][w];
+      for (int w = 0; w < kWarps; ++w) above += s_count[0][w];
       if (above + within == (uint32_t)a.budget) {  // those within are taken too
         threshold = low - 1u;
         need = 0;
         __syncthreads();
       } else if (within <= (uint32_t)kThreads) {
-        // list them, score a page with each warp, rank a page with each thread
-        for (int i = w0 + lane; i < w1; i += 32) {
-          const uint32_t key = s_key[i];
-          if (key >= low && key <= high) s_list[atomicAdd(&s_listed, 1u)] = i;
-          else s_key[i] = key > high ? kAlways : 0u;
-        }
-        __syncthreads();
-        for (uint32_t i = warp; i < within; i += kWarps) {
-          const uint32_t exact = Scores::rescore(a, p, (int)s_list[i]);
-          if (lane == 0) s_search.bin[i] = exact;
+        // score some heads of a page with each warp, rank a page with each thread
+        const int heads = max(1, min(a.group, (int)((within * a.group + kWarps - 1) / kWarps)));
+        const int parts = (a.group + heads - 1) / heads;
+        for (int i = warp; i < (int)within * parts; i += kWarps) {
+          const int x = i / parts, h0 = (i - x * parts) * heads;
+          const uint32_t exact = Scores::rescore(a, p, (int)s_list[x], h0, min(h0 + heads, a.group));
+          if (lane == 0) atomicMax(&s_search.bin[x], exact);
         }
         __syncthreads();
         if (tid < (int)within) {
@@ -583,11 +594,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
           s_key[page] = before < (uint32_t)a.budget ? kAlways : 0u;
         }
         __syncthreads();
-        threshold = kAlways - 1u;
+        threshold = high;
         need = 0;
       } else {
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-          const int i = i0 + lane;
+        // a stretch of pages for each warp, in steps of 32
+        const int stretch = ((held + kWarps - 1) / kWarps + 31) & ~31;
+        const int w0 = min(warp * stretch, held), w1 = min(w0 + stretch, held);
+        for (int j0 = w0; j0 < w1; j0 += 32) {
+          const int i = j0 + lane;
           const uint32_t key = i < w1 ? s_key[i] : 0u;
           const bool mid = i < w1 && key >= low && key <= high;
           if (i < w1 && !mid) s_key[i] = key > high ? kAlways : 0u;
@@ -595,8 +609,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
           while (left) {
             const int b = __ffs(left) - 1;
             left &= left - 1u;
-            const uint32_t exact = Scores::rescore(a, p, i0 + b);
-            if (lane == 0) s_key[i0 + b] = exact;
+            const uint32_t exact = Scores::rescore(a, p, j0 + b, 0, a.group);
+            if (lane == 0) s_key[j0 + b] = exact;
           }
         }
         __syncthreads();
@@ -605,19 +619,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     }
   }
 
-  // every key above the threshold and the first `need` equal to it, in order: a
-  // stretch of pages for each thread
-  const int mine = 4 * ((held + 4 * kThreads - 1) / (4 * kThreads));
-  const int i0 = min(tid * mine, held), i1 = min(i0 + mine, held);
-  auto each = [&](auto f) {
-    for (int i = i0; i < i1; i += 4) {
-      const uint4 k = *reinterpret_cast<const uint4*>(s_key + i);
-      f(i, k.x);
-      if (i + 1 < i1) f(i + 1, k.y);
-      if (i + 2 < i1) f(i + 2, k.z);
-      if (i + 3 < i1) f(i + 3, k.w);
-    }
-  };
+  // every key above the threshold and the first `need` equal to it, in order
   uint32_t count = 0;  // keys above (high half) and equal (low half): at most kMaxPages of each
   each([&](int, uint32_t key) { count += key > threshold ? 0x10000u : (key == threshold ? 1u : 0u); });
   uint32_t up = count;
