@@ -14,14 +14,14 @@
 //
 // Where the table (or the selection) has room for a few units a block only, a cluster
 // of up to 16 blocks takes each pair instead and joins through shared memory: one
-// launch, and no search for a share (see one_cluster).
+// launch, and no search for a share (see one_shape).
 //
 // What bounds it: K and V are read once, in bf16 and for up to 16 heads a group at
 // 93 to 99% of a plain copy's bandwidth (32768 keys x 32 heads x 128: 537 MB in 84
 // us, 6.4 TB/s; 131072 x 8 heads in e4m3, where the codes' widening doubles the
 // instructions for a byte: 268 MB in 49 us), beside some 6 us of start, partial
 // results and join.  Short contexts wait for a chain of latencies (launch, length,
-// page, keys, join): 16 keys take 4.5 to 6 us, 257 keys x 16 heads 5.2.  Groups of 32
+// page, keys, join): 16 keys take 3.7 to 4.8 us, 257 keys x 16 heads 5.0.  Groups of 32
 // heads wait for their instructions (268 MB in 70 us); sharing a ring between the warps
 // of a group took longer (77).
 #include <cooperative_groups.h>
@@ -49,6 +49,7 @@ constexpr int kChunk = 16;  // keys of one block; never straddles pages
 // 0, 67.5 with 2, 66 to 66.6 with 3 to 8).
 constexpr int kPairCost = 4;
 constexpr int kMaxGroup = 64;
+constexpr int kMostCluster = 16;
 
 struct DecodeArgs {
   const void *q, *k, *v;
@@ -149,7 +150,7 @@ struct FmaTile {
   // thread blocks of an SM.  Many warps hide the arithmetic better than deep rings (268 MB,
   // D = 128: as here 55 us; two blocks one deep 59, one block two deep 62).
   static constexpr int kSub = 1, kDepth = D == 128 ? 1 : 2, kCtas = NT == 1 ? 3 : 2;
-  static constexpr int kOneUnits = 3;    // of a block, at most, where a cluster takes a pair
+  static constexpr int kLineStart = 6;   // what the line's second launch costs: see one_shape
   static constexpr int kLines = D / 32;  // of a row
 
   __device__ static __forceinline__ int col(int h, int g, int e) { return 64 * h + 8 * g + e; }
@@ -279,7 +280,8 @@ struct MmaTile {
   // six deep 88.0, 65.2; e4m3 in steps of 16 keys, four deep, 54.3.  Rows of 64 bytes (e4m3,
   // D = 64), the most instructions for a byte, take a third block: 268 MB 51 us, else 58.
   static constexpr int kSub = 256 / kRowBytes;
-  static constexpr int kDepth = 2, kOneUnits = 4;
+  static constexpr int kDepth = 2;
+  static constexpr int kLineStart = 12;  // what the line's second launch costs: see one_shape
   static constexpr int kCtas = NT == 1 && kRowBytes == 64 ? 3 : 2;
   // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
   // ends at 2^-24, which must be far below the largest weight of a long context.
@@ -784,10 +786,10 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) oo[e] *= v_unit;
-      if constexpr (ONE) {  // in place: no other thread reads these four
+      if (ONE && ranks > 1) {  // in place: no other thread reads these four
         *reinterpret_cast<float4*>(&s_buf[hw * HT + hh][d]) = make_float4(oo[0], oo[1], oo[2], oo[3]);
         if (d == 0) s_ml[head] = make_float2(mm, ll);
-      } else if (whole) {
+      } else if (ONE || whole) {
         finish<4>(a, (size_t)r * a.Hq + (size_t)h * a.group + head, D, d, oo, mm, ll);
       } else {
         const size_t at = (size_t)slot * a.group + head;
@@ -795,6 +797,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
         if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mm, ll);
       }
     }
+    if (ONE && ranks == 1) break;
     if constexpr (ONE) {
       // every block joins a share of the outputs
       cg::cluster_group cluster = cg::this_cluster();
@@ -805,19 +808,27 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
         float2* ml = &s_ml[head];
         float4* from = reinterpret_cast<float4*>(&s_buf[head / HT * HT + head % HT][d]);
         float mm = kNothing, ll = 0.f, oo[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int c = 0; c < ranks; ++c) mm = fmaxf(mm, cluster.map_shared_rank(ml, c)->x);
-#pragma unroll 8
-        for (int c = 0; c < ranks; ++c) {
-          const float2 p = *cluster.map_shared_rank(ml, c);
-          const float4 x = *cluster.map_shared_rank(from, c);
-          const float f = exp2_fast(p.x - mm);
-          ll = fmaf(f, p.y, ll);
-          oo[0] = fmaf(f, x.x, oo[0]), oo[1] = fmaf(f, x.y, oo[1]), oo[2] = fmaf(f, x.z, oo[2]), oo[3] = fmaf(f, x.w, oo[3]);
+        float2 p[kMostCluster];  // all asked for at once
+        float4 x[kMostCluster];
+#pragma unroll
+        for (int c = 0; c < kMostCluster; ++c) {
+          p[c] = make_float2(kNothing, 0.f), x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < ranks) p[c] = *cluster.map_shared_rank(ml, c), x[c] = *cluster.map_shared_rank(from, c);
+        }
+#pragma unroll
+        for (int c = 0; c < kMostCluster; ++c) mm = fmaxf(mm, p[c].x);
+#pragma unroll
+        for (int c = 0; c < kMostCluster; ++c) {
+          const float f = exp2_fast(p[c].x - mm);
+          ll = fmaf(f, p[c].y, ll);
+          oo[0] = fmaf(f, x[c].x, oo[0]), oo[1] = fmaf(f, x[c].y, oo[1]), oo[2] = fmaf(f, x[c].z, oo[2]), oo[3] = fmaf(f, x[c].w, oo[3]);
         }
         finish<4>(a, (size_t)r * a.Hq + (size_t)h * a.group + head, D, d, oo, mm, ll);
       }
-      cluster.sync();  // no block leaves while its results are read
+      // No block leaves while its results are read.  They have been when a thread arrives, and
+      // nothing here is for the others to see: no release, which would wait for the outputs.
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      cluster.barrier_wait();
     } else if (x0 == 0) {
       if (!whole) {  // the block that holds the pair's last unit
         const int last = base + (h + 1) * w_pair - 1, long_ones = more * (each + 1);
@@ -917,21 +928,57 @@ size_t ws_part_o(int grid, int group, int D) { return (size_t)2 * grid * group *
 size_t ws_part_ml(int grid, int group) { return ((size_t)2 * grid * group * 2 * sizeof(float) + 15) & ~(size_t)15; }
 constexpr int kMostCtas = 3;  // blocks of an SM, over all variants
 
-// Blocks of the cluster that takes each of `pairs` pairs of up to `units` units, when all
-// of them fit on the GPU at once (`places`) and no block has more than `most` units: 0 if not.
-// With more units a block its ring idles at the start and end of a pair, and pairs of
-// different lengths end at different times, which the line levels.  Measured, clusters |
-// line (us): bf16, 8 heads, 257 keys 5.2 | 6.7, 1024 6.2 | 7.5, 4096 (four units a block)
-// 8.7 | 9.0; 32 requests x 4 heads of 257 keys 8.7 | 10.4; fp32, 8 heads, 1024 keys 6.5 |
-// 8.1, four units a block 12.4 | 11.0.  Clusters of up to 8 blocks: 2048 keys 7.6 and with
-// 16 6.5 (2 heads).
-constexpr unsigned kMostCluster = 16;
-unsigned one_cluster(long long pairs, long long units, long long places, int most) {
-  unsigned cluster = 1;
-  while (cluster < kMostCluster && cluster < units && pairs * cluster * 2 <= places) cluster *= 2;
-  return pairs * cluster <= places && units <= (long long)most * cluster ? cluster : 0;
+// Clusters of `cluster` blocks that the current device runs at once, when it is empty.
+template <typename Kernel>
+int clusters_at_once(Kernel* kernel, int threads, int smem, int cluster) {
+  cudaLaunchAttribute attr[1] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+  cudaGetLastError();
+  return 0;
 }
 
+// How a cluster for each pair would run: blocks of a cluster, blocks of an SM, and what it
+// costs in quarters of a unit of keys.
+struct OneShape {
+  int cluster, per_sm, cost;
+};
+// A block's units cost 5 each, sharing an SM 4 for each block of it, and a cluster of one
+// block saves the join: the choice that is best or within 5% of it at 1 to 200 pairs of 64
+// to 4096 keys in bf16, e4m3 and fp32 (bf16, us: 16 pairs of 513 keys in clusters of 4, 8,
+// 16 blocks 6.4, 6.1, 6.5; 96 pairs of 257 in clusters of 1, 2, 4 6.8, 7.7, 7.4).  `room`
+// says how many clusters of 2^i blocks run at once; more blocks of an SM than that takes
+// would crowd some SMs (32 clusters of 8: 7.0 us with two blocks of an SM, 7.7 with three).
+// At most kOneUnits units a block: requests shorter than the table is wide leave clusters
+// idle, which the line levels.
+// Clusters | line (us): bf16, 8 heads of 257 keys 5.0 | 6.7, of 1024 5.6 | 7.4, of 4096 8.2 |
+// 9.0; 32 requests x 4 heads of 257 keys 6.8 | 10.4, of 512 9.9 | 13.0; e4m3, the same of 1024
+// keys 11.6 | 15; fp32, 8 heads of 1024 keys 6.1 | 8.1, of 4096 12.1 | 10.9.
+constexpr int kOneUnits = 5, kNoJoin = 8;
+template <typename Room>
+OneShape one_shape(long long pairs, long long units, Room room) {
+  OneShape best = {0, 0, 1 << 30};
+  for (int i = 0; (1 << i) <= kMostCluster && (i == 0 || (1 << (i - 1)) < units); ++i) {
+    const long long each = (units + (1 << i) - 1) >> i;
+    if (each > kOneUnits) continue;
+    for (int per_sm = 1; per_sm <= kMostCtas; ++per_sm)
+      if (room(per_sm, i) >= pairs) {
+        const int cost = (int)(5 * each + 4 * per_sm) - (i == 0 ? kNoJoin : 0);
+        if (cost < best.cost) best = {1 << i, per_sm, cost};
+        break;
+      }
+  }
+  return best;
+}
 
 template <typename Tile, int D, int NT>
 int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
@@ -946,20 +993,34 @@ int launch_tile(DecodeArgs a, cudaStream_t s, long long max_units, char* ws) {
   const long long pairs = (long long)a.R * a.Hkv, places = decode_grid(Tile::kCtas, 1LL << 40);
   const long long listed = a.pages ? std::min(a.budget, a.max_pages) : a.max_pages;
   const long long pair_units = ((listed << a.shift) + kUnit - 1) / kUnit;
-  const unsigned cluster = one_cluster(pairs, pair_units, places, Tile::kOneUnits);
-  if (cluster) {
-    static std::atomic<unsigned long long> done{0};
-    auto* kernel = decode_kernel<Tile, D, NT, true>;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
-    if (!(done.load() & (1ull << dev)) &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  // shared memory that leaves an SM room for 1, 2 or 3 blocks
+  constexpr int kOneBytes[kMostCtas] = {120 * 1024, 80 * 1024, kBytes};
+  static_assert(kBytes <= 72 * 1024, "three blocks of an SM");
+  auto* one = decode_kernel<Tile, D, NT, true>;
+  static std::atomic<unsigned long long> one_done{0};
+  static std::atomic<int> known[64][kMostCtas][5];  // clusters at once, and one more
+  if (pair_units <= kOneUnits * kMostCluster) {
+    if (!(one_done.load() & (1ull << dev)) &&
+        cudaFuncSetAttribute(one, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return -1;
-    if (!smem_attr_once(kernel, kBytes, done)) return -1;
-    prof_begin(kKDecode, s);
-    e = launch_chained(kernel, dim3((unsigned)pairs * cluster), kThreads, kBytes, cluster, s, a, k_map, v_map);
-    prof_end(kKDecode, s);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
+    if (!smem_attr_once(one, kOneBytes[0], one_done)) return -1;
+    const OneShape shape = one_shape(pairs, pair_units, [&](int per_sm, int i) {
+      std::atomic<int>& k = known[dev][per_sm - 1][i];
+      if (k.load() == 0) k.store(1 + clusters_at_once(one, kThreads, kOneBytes[per_sm - 1], 1 << i));
+      return k.load() - 1;
+    });
+    // the line: two launches and a join, kPairCost for each pair, every block the same
+    const long long line = pairs * (pair_units + kPairCost), sms = places / Tile::kCtas;
+    const long long line_cost = 5 * std::max(line, places) / places + 4 * std::min<long long>(Tile::kCtas, (line + sms - 1) / sms);
+    if (shape.cluster && shape.cost < line_cost + Tile::kLineStart) {
+      prof_begin(kKDecode, s);
+      e = launch_chained(one, dim3((unsigned)(pairs * shape.cluster)), kThreads, kOneBytes[shape.per_sm - 1],
+                         shape.cluster, s, a, k_map, v_map);
+      prof_end(kKDecode, s);
+      return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 1 : -1;
+    }
   }
   static std::atomic<unsigned long long> done{0};
   if (!smem_attr_once(decode_kernel<Tile, D, NT, false>, kBytes, done)) return -1;
