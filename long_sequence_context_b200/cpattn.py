@@ -576,7 +576,7 @@ def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, 
     and free-page state (new tensors, or lens_out / free_state_out, which may be
     lens and free_state themselves), the first new token of each request, the slot
     of each new token (`capacity` of them, -1 behind the last) and 0 or PLAN_* bits
-    (then nothing changed)."""
+    (then nothing changed).  New tensors other than slots may share an allocation."""
     if lens_out is None and free_state_out is None and workspace is None and stream is None:
         r = _calls.cache_plan(lens, delta, block_table, free_ring, free_state, page_size, capacity)
         if r is not None:

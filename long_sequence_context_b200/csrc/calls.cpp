@@ -55,6 +55,13 @@ void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIn
 at::Tensor empty(std::initializer_list<int64_t> sizes, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
 }
+// `n` elements of one allocation from element `at` on, as a tensor of one dimension.
+at::Tensor part(const at::Tensor& all, int64_t at, int64_t n) {
+  const int64_t one = 1;
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(c10::IntArrayRef(n), c10::IntArrayRef(one), at);
+  return t;
+}
 PyObject* answer(int status, std::initializer_list<at::Tensor> outputs) {
   PyObject* r = PyTuple_New((Py_ssize_t)outputs.size() + 1);
   if (!r) return nullptr;
@@ -120,9 +127,11 @@ PyObject* cache_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!sized(lens, {R}) || !sized(delta, {R}) || !ring || !sized(state, {2}) || !fits_int(R) || !fits_int(width) ||
       !fits_int(ring->size(0)) || !current(dev))
     Py_RETURN_NONE;
-  const at::Tensor lens_out = empty({R}, at::kInt, dev), state_out = empty({2}, at::kInt, dev),
-                   cu = empty({R + 1}, at::kInt, dev), verdict = empty({1}, at::kInt, dev),
-                   slots = empty({capacity}, at::kLong, dev);
+  // the small outputs are one allocation: five take 1 us longer
+  const int64_t stretch = (R + 4) / 4 * 4;  // of R + 1 elements, 16-byte aligned
+  const at::Tensor small = empty({2 * stretch + 8}, at::kInt, dev), slots = empty({capacity}, at::kLong, dev);
+  const at::Tensor lens_out = part(small, 0, R), cu = part(small, stretch, R + 1), state_out = part(small, 2 * stretch, 2),
+                   verdict = part(small, 2 * stretch + 4, 1);
   const size_t need = f_plan_ws((int)R, (long)capacity);
   at::Tensor ws;
   if (need) ws = empty({(int64_t)need}, at::kByte, dev);

@@ -801,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
     if constexpr (ONE) {
       // every block joins a share of the outputs
       cg::cluster_group cluster = cg::this_cluster();
+      __syncwarp();
       cluster.sync();
       const int n = a.group * (D / 4), share = (n + ranks - 1) / ranks;
       for (int i = rank * share + tid; i < min(n, (rank + 1) * share); i += kThreads) {
@@ -827,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
       }
       // No block leaves while its results are read.  They have been when a thread arrives, and
       // nothing here is for the others to see: no release, which would wait for the outputs.
+      __syncwarp();
       asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
       cluster.barrier_wait();
     } else if (x0 == 0) {

@@ -23,8 +23,8 @@
 // the pages.  A page's bounds are read once; what bounds the kernel is the
 // chain of latencies from the lengths over the page table and the bounds to the
 // search, so the pages are spread over as many blocks as the device holds at once.
-// Measured (8 kv heads, 4 query heads each, D = 128, us): 2048 pages 12.1, 8192
-// pages 25.6 (33.8 with every page scored in 64 bits), 16 x 8192 pages 118 (197).
+// Measured (8 kv heads, 4 query heads each, D = 128, us): 2048 pages 11.0, 8192
+// pages 24.4 (33.8 with every page scored in 64 bits), 16 x 8192 pages 118 (197).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   const int held = (int)((len + (1 << a.shift) - 1) >> a.shift);
   if (held <= a.budget) {  // everything is selected (the whole cluster leaves here)
     for (int j = rank * kThreads + tid; j < a.budget; j += ranks * kThreads) out[j] = j < held ? j : -1;
+    __syncwarp();
     cluster.barrier_wait();
     return;
   }
