@@ -358,7 +358,7 @@ int cpattn_gemm(const void* A, const void* B, const void* bias, void* C, int M, 
 /* Bits of a plan's verdict. */
 enum {
     CPATTN_PLAN_SHORT = 1,      /* fewer free pages than the step needs */
-    CPATTN_PLAN_BAD_LENGTH = 2, /* a length would fall below 0 or pass max_pages * page_size */
+    CPATTN_PLAN_BAD_LENGTH = 2, /* a length is, or would come to be, below 0 or above max_pages * page_size */
     CPATTN_PLAN_CAPACITY = 4,   /* more new tokens than `capacity` slots */
     CPATTN_PLAN_BAD_STATE = 8   /* the free pages' books do not balance */
 };

@@ -64,8 +64,9 @@ __device__ __forceinline__ long long pages_of(long long n, int shift) { return (
 
 // What request r asks for: new tokens, pages taken, pages returned.
 __device__ __forceinline__ Three request_of(const PlanArgs& a, int r, int* bad) {
-  const long long n = a.lens[r], after = n + a.delta[r];
-  if (n < 0 || after < 0 || after > ((long long)a.max_pages << a.shift)) {
+  const long long n = a.lens[r], after = n + a.delta[r], room = (long long)a.max_pages << a.shift;
+  // n too: the pages that a request gives back are read from its row of the table
+  if (n < 0 || n > room || after < 0 || after > room) {
     *bad |= kBadLength;
     return {0, 0, 0};
   }

@@ -21,7 +21,7 @@ def plan(lens, delta, table, ring, state, page_size, capacity):
     R, width = table.shape
     verdict, need, back, tokens = 0, 0, 0, 0
     for n, d in zip(lens, delta):
-        if n < 0 or n + d < 0 or n + d > width * page_size:
+        if not 0 <= n <= width * page_size or not 0 <= n + d <= width * page_size:
             verdict |= BAD_LENGTH
             continue
         more = pages_of(n + d, page_size) - pages_of(n, page_size)

@@ -62,3 +62,11 @@ def test_selection_lists_every_page_within_the_budget_and_breaks_ties_low():
         j = [int(x) for x in c["table"][0][:5]].index(p)
         rows = pu.values(c["k"])[p, 0, :min(16, 70 - 16 * j)]
         assert paged.scores(q, lo, hi) >= (rows @ q.T).max() - 1e-12
+
+
+def test_plan_refuses_a_length_above_its_table():
+    table, ring = np.array([[0, 1], [2, 3]]), [4, 5, 6, 7]
+    for lens, delta in [([32, 70], [0, -70]), ([33, 5], [-33, 0]), ([32, 2 ** 31 - 1], [0, -(2 ** 31 - 33)])]:
+        out = paged.plan(lens, delta, table, ring, [0, 2], 16, 4)
+        assert out[6] == paged.BAD_LENGTH and out[0] == lens and out[2] == ring and np.array_equal(out[1], table)
+    assert paged.plan([32, 32], [0, -32], table, ring + [0] * 4, [0, 2], 16, 4)[6] == 0
