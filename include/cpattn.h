@@ -380,7 +380,9 @@ enum {
  *   slots          [capacity] int64: slot of every new token, -1 behind the last
  *   verdict        int32[1]: 0, or CPATTN_PLAN_* bits; then nothing changes:
  *                  lens_out = lens, free_state_out = free_state, cu_new 0, slots -1
- * Pages returned by a call can be taken from the next call on.
+ * Pages returned by a call can be taken from the next call on.  Page numbers in the
+ * table and the ring are the caller's: one outside of the pool that is taken or
+ * returned is recorded (CPATTN_ERR_PAGE) and passed on, and its tokens get slot -1.
  * Workspace: cpattn_cache_plan_workspace_bytes(R, capacity), 16-byte aligned;
  * contents on entry are ignored; calls that can overlap on the GPU need one each.
  * 0 (and NULL) for steps of up to 1024 requests and 2048 tokens.

@@ -198,6 +198,13 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
     cell = (size_t)r * a.max_pages + first + (k - at[r]);
     place = ring_at((back ? ring_at((long long)head + count, a.num_pages) : head) + (long long)k, a.num_pages);
   };
+  // A number outside of the pool is passed on as it is, so that the books still count, and
+  // reported: nothing ever follows it.  (Of the pages taken the new tokens report it.)
+  auto put_page = [&](bool back, size_t cell, int place, int page) {
+    if (back && (unsigned)page >= (unsigned)a.num_pages) atomicOr(a.err, kErrPage);
+    if (back) a.ring[place] = page;
+    else a.table[cell] = page;
+  };
   auto move = [&](int total, const int32_t* at, bool back) {
     // several at a time while there are: one block may have to return the pages of a long context
     constexpr int kAhead = 4;
@@ -211,18 +218,14 @@ __device__ __forceinline__ void plan_items(const PlanArgs& a, const Prefix& p, l
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) page[x] = back ? a.table[cell[x]] : a.ring[place[x]];
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        if (back) a.ring[place[x]] = page[x];
-        else a.table[cell[x]] = page[x];
-      }
+      for (int x = 0; x < kAhead; ++x) put_page(back, cell[x], place[x], page[x]);
     }
 #pragma unroll 1
     for (; i < total; i += n) {
       size_t cell;
       int place;
       find_page((int)i, at, back, cell, place);
-      if (back) a.ring[place] = a.table[cell];
-      else a.table[cell] = a.ring[place];
+      put_page(back, cell, place, back ? a.table[cell] : a.ring[place]);
     }
   };
   move(pops, p.pop_at, false);

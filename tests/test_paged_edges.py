@@ -44,3 +44,25 @@ def test_plan_refuses_a_length_above_its_table(cp, R, in_place):
             assert all(torch.equal(x, y) for x, y in zip((around, ring, state, lens), keep))
             assert torch.equal(out[0], keep[3]) and torch.equal(out[1], keep[2])
             assert out[2].count_nonzero() == 0 and torch.all(out[3] == -1)
+
+
+@pytest.mark.parametrize("many", [1, 300])
+def test_plan_reports_pages_outside_of_the_pool_that_come_back(cp, many):
+    """The books count them all the same, and the next request that takes one gets no slots in it."""
+    P, width, num_pages = 16, 2 * many, 4 * many + 2
+    table = torch.arange(2 * width, dtype=torch.int32).view(2, width)
+    table[1, 3 % width], table[1, width - 1] = -1, num_pages
+    ring, state = torch.full((num_pages,), -1, dtype=torch.int32), [0, 0]
+    t, r = table.cuda(), ring.cuda()
+    lens, delta = [P * width, P * width], [0, -P * width]
+    out = cp.cache_plan(_i32(lens), _i32(delta), t, r, _i32(state), P, 0)
+    want = paged.plan(lens, delta, table.numpy(), ring.tolist(), state, P, 0)
+    assert cp.sync_status() == cp.ERR_PAGE and cp.sync_status() == cp.OK
+    assert out[4].item() == want[6] == 0
+    assert r.tolist() == want[2] and out[1].tolist() == want[3] and torch.equal(t.cpu(), table)
+    n = P * width
+    out = cp.cache_plan(out[0], _i32([0, n]), t, r, out[1], P, n)
+    assert cp.sync_status() == cp.ERR_PAGE and out[4].item() == 0
+    pages = table[1].long()
+    slots = (pages[:, None] * P + torch.arange(P)).masked_fill(((pages < 0) | (pages >= num_pages))[:, None], -1)
+    assert torch.equal(out[3].cpu(), slots.view(-1))
