@@ -675,7 +675,9 @@ __global__ void __launch_bounds__(kThreads, Tile::kCtas)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        unit[nt][i] = scale_log2 * (sizeof(CT) == 1 ? s_unit[hg * HT + nt * 8 + 2 * t + i] : 1.f);
+        // never 0: a masked score is -inf, and 0 times that is NaN.  (A product below 2^-149 takes
+        // every score of a head, at most 2^31 in half precision, to 0 all the same.)
+        unit[nt][i] = fmaxf(scale_log2 * (sizeof(CT) == 1 ? s_unit[hg * HT + nt * 8 + 2 * t + i] : 1.f), 0x1p-149f);
 
     for (int i = 0; i < n_mine; ++i, ++done) {
       const int slot = (int)(done % kDepth);

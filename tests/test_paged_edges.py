@@ -66,3 +66,28 @@ def test_plan_reports_pages_outside_of_the_pool_that_come_back(cp, many):
     pages = table[1].long()
     slots = (pages[:, None] * P + torch.arange(P)).masked_fill(((pages < 0) | (pages >= num_pages))[:, None], -1)
     assert torch.equal(out[3].cpu(), slots.view(-1))
+
+
+@pytest.mark.parametrize("width", [10, 2048])
+@pytest.mark.parametrize("amax", [5.0, 0.05])
+@pytest.mark.parametrize("exponent", [-133, -128, -126, -120, -110])
+def test_decode_tiny_queries_at_the_ordinary_scale(cp, exponent, amax, width):
+    """Scores next to 0 are a mean of V, also where the masked rows of a step stand beside them."""
+    c = pu.make_cache([300, 40, 7, 64, 0], 6, 2, 128, 32, "e4m3", seed=15, width=width)
+    c["q"] = (c["q"].double() * 2.0 ** exponent).to(c["q"].dtype)
+    c["amax"] = torch.tensor([amax, 0.9 * amax])
+    d = pu.on_gpu(c)
+    o, lse = cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], kv_amax=d["amax"])
+    assert cp.sync_status() == cp.OK
+    pu.assert_decode(o, lse, pu.reference(c, 128 ** -0.5), 128, 128 ** -0.5, 300, "e4m3")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3"])
+@pytest.mark.parametrize("width", [10, 2048])
+def test_decode_smallest_scale(cp, kind, width):
+    c = pu.make_cache([300, 40, 7], 6, 2, 128, 32, kind, seed=17, width=width)
+    scale = 2.0 ** -149
+    d = pu.on_gpu(c)
+    o, lse = cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], kv_amax=d["amax"], scale=scale)
+    assert cp.sync_status() == cp.OK
+    pu.assert_decode(o, lse, pu.reference(c, scale), 128, scale, 300, kind)
