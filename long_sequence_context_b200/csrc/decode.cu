@@ -145,7 +145,7 @@ template <int D, int NT>
 struct FmaTile {
   using CT = float;
   static constexpr int kQueryBytes = D * 4;  // shared memory of one head's query
-  static constexpr float kLift = 0.f, kSlack = 8.f;
+  static constexpr float kLift = -4.f, kSlack = 4.f;  // weights up to 1: see MmaTile
   // Blocks of 16 keys a warp takes at a time, how many times that it has under way, and
   // thread blocks of an SM.  Many warps hide the arithmetic better than deep rings (268 MB,
   // D = 128: as here 55 us; two blocks one deep 59, one block two deep 62).
@@ -283,9 +283,10 @@ struct MmaTile {
   static constexpr int kDepth = 2;
   static constexpr int kLineStart = 12;  // what the line's second launch costs: see one_shape
   static constexpr int kCtas = NT == 1 && kRowBytes == 64 ? 3 : 2;
-  // The largest weight lies between 2^kLift and 2^(kLift + kSlack) times 1: half precision
-  // ends at 2^-24, which must be far below the largest weight of a long context.
-  static constexpr float kLift = kHalf ? 14.f : 0.f, kSlack = kHalf ? 1.f : 8.f;
+  // The largest weight lies between 2^kLift and 2^(kLift + kSlack): half precision ends at
+  // 2^-24, which must be far below the largest weight of a long context.  bf16 reaches as far
+  // as fp32, so there no weight is above 1 and the sums overflow only where n max|v| does.
+  static constexpr float kLift = kHalf ? 14.f : -4.f, kSlack = kHalf ? 1.f : 4.f;
 
   __device__ static __forceinline__ int col(int h, int g, int e) {
     return kHalf ? D / 8 * g + 8 * h + e : 64 * h + 8 * g + e;

@@ -91,3 +91,25 @@ def test_decode_smallest_scale(cp, kind, width):
     o, lse = cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], kv_amax=d["amax"], scale=scale)
     assert cp.sync_status() == cp.OK
     pu.assert_decode(o, lse, pu.reference(c, scale), 128, scale, 300, kind)
+
+
+@pytest.mark.parametrize("width", [5, 4096])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("D,group", [(64, 1), (128, 1), (64, 9), (128, 40)])
+def test_decode_values_as_large_as_their_sum_allows(cp, kind, D, group, width):
+    """64 keys of weight 1 and 256 of less, |v| up to 2^122: a weighted sum stays below 2^128
+    (2^122 (64 + 24)), and does so only while no weight is above 1.  Scores rise from page to
+    page, by less than what makes the reference of the weights follow."""
+    n, P, heads = 320, 64, 300
+    c = pu.make_cache([n], group * heads, heads, D, P, kind, seed=16, width=width)
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"][..., 0] = 1.0
+    for j in range(5):
+        page = c["table"][0, j].long()
+        c["k"][page] = 0
+        c["k"][page, :, :, 0] = 1.3 * j
+        c["v"][page] = (c["v"][page].float().abs().clamp(max=8.0) * 2.0 ** 119).to(c["v"].dtype)
+    d = pu.on_gpu(c)
+    o, lse = cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], scale=1.0)
+    assert cp.sync_status() == cp.OK
+    pu.assert_decode(o, lse, pu.reference(c, 1.0), D, 1.0, n, kind)
