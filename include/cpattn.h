@@ -403,8 +403,9 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
  *                  saves them ([H][S][D]) have token stride D and head stride S * D
  *   k_bounds       kept up to date, or NULL.  A row in a page's first slot starts
  *                  the page's bounds afresh.  With k_bounds, the new tokens of one
- *                  page must stand next to one another and ascend, as
- *                  cpattn_cache_plan lists them.  Bounds do not shrink when tokens are
+ *                  page must stand next to one another, as cpattn_cache_plan lists
+ *                  them: no token of another page and no skipped one between them
+ *                  (their slots may leave gaps).  Bounds do not shrink when tokens are
  *                  taken back: they still cover the rows that were there.  NaN
  *                  keys are left out of them
  * A slot may appear once only.  N = 0 does nothing.

@@ -633,7 +633,8 @@ def _rows(t, name, shape, dtype, like):
 def cache_append_(k_new, v_new, slots, k_cache, v_cache, k_bounds=None, kv_amax=None, stream=None):
     """New rows into a paged cache (in place): k_new, v_new [N, kv_heads, D] with
     contiguous columns (views of [kv_heads, N, D] too), slots [N] int64 (negative:
-    skipped).  k_bounds [num_pages, kv_heads, 2, D] is kept up to date when given."""
+    skipped).  k_bounds [num_pages, kv_heads, 2, D] is kept up to date when given;
+    the new tokens of one page must then stand next to one another in slots."""
     if stream is None:
         r = _calls.cache_append(k_new, v_new, slots, k_cache, v_cache, k_bounds, kv_amax)
         if r is not None:

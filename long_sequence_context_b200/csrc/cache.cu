@@ -313,10 +313,12 @@ __device__ __forceinline__ void put(CT* p, float (&f)[V], float s) {
 constexpr int kAppendWarps = 4;
 constexpr int kTile = 32;  // tokens whose slots one block looks at
 
-// The new rows fall into runs: tokens next to one another in one page.  A warp
-// takes a run of one kv head, copies it with kAhead rows' loads under way and
-// reduces its keys.  Blocks (x: 32 tokens; y: a share of their runs and heads)
-// find the runs that begin in their tokens by a vote over the slots.
+// The new rows fall into stretches: tokens next to one another in one page.  A warp
+// takes a stretch of one kv head and copies its runs of consecutive slots one after
+// another, with kAhead rows' loads under way, reduces their keys and writes the page's
+// bounds once: no other warp touches these.  Blocks (x: 32 tokens; y: a share of their
+// stretches and heads) find the stretches that begin in their tokens by a vote over the
+// slots.
 template <typename IT, typename CT, int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a) {
   constexpr int V = 16 / (int)sizeof(IT);  // elements of a lane
@@ -331,62 +333,72 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   if (lane == 0) before = t0 > 0 ? a.slots[t0 - 1] : -1;
   const bool bad = mine >= a.n_slots;
   if (bad && warp == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPage);
-  const bool first = mine >= 0 && !bad && ((mine & page_mask) == 0 || before != mine - 1);
-  const uint32_t runs = __ballot_sync(0xffffffffu, first);
-  const int nth = __popc(runs & ((1u << lane) - 1u));
+  const bool first = mine >= 0 && !bad && before >> a.shift != mine >> a.shift;
+  const uint32_t stretches = __ballot_sync(0xffffffffu, first);
+  const int nth = __popc(stretches & ((1u << lane) - 1u));
   const float ks = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax[0]) : 1.f;
   const float vs = sizeof(CT) == 1 ? e4m3_scale(a.kv_amax[1]) : 1.f;
   const int sub = lane / kLanes, d = lane % kLanes * V;
 
-  const int items = __popc(runs) * a.Hkv;
+  const int items = __popc(stretches) * a.Hkv;
   for (int item = blockIdx.y * kAppendWarps + warp; item < items; item += gridDim.y * kAppendWarps) {
-    const int run = item / a.Hkv, h = item % a.Hkv;
-    const int from = __ffs(__ballot_sync(0xffffffffu, first && nth == run)) - 1;
-    const long long t = t0 + from, slot = __shfl_sync(0xffffffffu, mine, from);
-    const int off = (int)(slot & page_mask);
-    // the run's length: up to the page's end
-    const int most = (int)min((long long)(page_mask + 1 - off), a.N - t);
-    int len = 1;
-    for (int i = 1; i < most; i += 32) {
-      const bool on = i + lane < most && a.slots[t + i + lane] == slot + i + lane;
-      const uint32_t gap = ~__ballot_sync(0xffffffffu, on);
-      len = i + (gap ? __ffs(gap) - 1 : 32);
-      if (gap) break;
-    }
-    const IT* k = static_cast<const IT*>(a.k) + t * a.k_tok + h * a.k_head + d;
-    const IT* v = static_cast<const IT*>(a.v) + t * a.v_tok + h * a.v_head + d;
-    const size_t at = ((((size_t)(slot >> a.shift) * a.Hkv + h) << a.shift) + off) * D + d;
-    CT* kc = static_cast<CT*>(a.k_cache) + at;
-    CT* vc = static_cast<CT*>(a.v_cache) + at;
+    const int stretch = item / a.Hkv, h = item % a.Hkv;
+    const int from = __ffs(__ballot_sync(0xffffffffu, first && nth == stretch)) - 1;
+    long long t = t0 + from, slot = __shfl_sync(0xffffffffu, mine, from);
+    const long long page = slot >> a.shift;
+    bool fresh = false;  // the page's first row is among them
     float lo[V], hi[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) lo[e] = INFINITY, hi[e] = -INFINITY;
-    for (int i0 = sub; i0 < len; i0 += kRows * kAhead) {
-      uint32_t kw[kAhead][4], vw[kAhead][4];
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        const int i = i0 + x * kRows;
-        if (i < len) {
-          load_words<16>(k + i * a.k_tok, kw[x]);
-          load_words<16>(v + i * a.v_tok, vw[x]);
+    while (slot >> a.shift == page) {
+      const int off = (int)(slot & page_mask);
+      // the run's length, up to the page's end, and the slot behind it
+      const int most = (int)min((long long)(page_mask + 1 - off), a.N - t);
+      int len;
+      long long next;
+      for (int i = 1;; i += 32) {
+        const long long x = t + i + lane < a.N ? a.slots[t + i + lane] : -1;
+        const uint32_t gap = ~__ballot_sync(0xffffffffu, i + lane < most && x == slot + i + lane);
+        if (gap) {
+          len = i + __ffs(gap) - 1;
+          next = __shfl_sync(0xffffffffu, x, __ffs(gap) - 1);
+          break;
         }
       }
+      const IT* k = static_cast<const IT*>(a.k) + t * a.k_tok + h * a.k_head + d;
+      const IT* v = static_cast<const IT*>(a.v) + t * a.v_tok + h * a.v_head + d;
+      const size_t at = ((((size_t)page * a.Hkv + h) << a.shift) + off) * D + d;
+      CT* kc = static_cast<CT*>(a.k_cache) + at;
+      CT* vc = static_cast<CT*>(a.v_cache) + at;
+      for (int i0 = sub; i0 < len; i0 += kRows * kAhead) {
+        uint32_t kw[kAhead][4], vw[kAhead][4];
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        const int i = i0 + x * kRows;
-        if (i < len) {
-          float f[V], g[V];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            Unpack<IT>::word(kw[x][w], f + w * Unpack<IT>::kPerWord);
-            Unpack<IT>::word(vw[x][w], g + w * Unpack<IT>::kPerWord);
+        for (int x = 0; x < kAhead; ++x) {
+          const int i = i0 + x * kRows;
+          if (i < len) {
+            load_words<16>(k + i * a.k_tok, kw[x]);
+            load_words<16>(v + i * a.v_tok, vw[x]);
           }
-          put<CT, V>(kc + (size_t)i * D, f, ks);
-          put<CT, V>(vc + (size_t)i * D, g, vs);
+        }
 #pragma unroll
-          for (int e = 0; e < V; ++e) lo[e] = fminf(lo[e], f[e]), hi[e] = fmaxf(hi[e], f[e]);
+        for (int x = 0; x < kAhead; ++x) {
+          const int i = i0 + x * kRows;
+          if (i < len) {
+            float f[V], g[V];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              Unpack<IT>::word(kw[x][w], f + w * Unpack<IT>::kPerWord);
+              Unpack<IT>::word(vw[x][w], g + w * Unpack<IT>::kPerWord);
+            }
+            put<CT, V>(kc + (size_t)i * D, f, ks);
+            put<CT, V>(vc + (size_t)i * D, g, vs);
+#pragma unroll
+            for (int e = 0; e < V; ++e) lo[e] = fminf(lo[e], f[e]), hi[e] = fmaxf(hi[e], f[e]);
+          }
         }
       }
+      fresh |= off == 0;
+      t += len, slot = next;
     }
     if (!a.bounds) continue;
 #pragma unroll
@@ -397,8 +409,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
         hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
       }
     if (sub != 0) continue;
-    CT* b = static_cast<CT*>(a.bounds) + ((size_t)(slot >> a.shift) * a.Hkv + h) * 2 * D + d;
-    if (off > 0) {  // the page held rows before: the first row of a page starts its bounds afresh
+    CT* b = static_cast<CT*>(a.bounds) + ((size_t)page * a.Hkv + h) * 2 * D + d;
+    if (!fresh) {  // the page held rows before: its first row starts its bounds afresh
       constexpr int W = V * (int)sizeof(CT) / 4;
       uint32_t w[2][W];
 #pragma unroll

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import paged
+from oracle import fp8, paged
 from tests import paged_util as pu
 
 pytestmark = pytest.mark.gpu
@@ -113,3 +113,40 @@ def test_decode_values_as_large_as_their_sum_allows(cp, kind, D, group, width):
     o, lse = cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], scale=1.0)
     assert cp.sync_status() == cp.OK
     pu.assert_decode(o, lse, pu.reference(c, 1.0), D, 1.0, n, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3"])
+@pytest.mark.parametrize("Hkv,D,P", [(1, 64, 16), (3, 128, 64)])
+def test_append_bounds_of_pages_whose_new_tokens_leave_gaps(cp, kind, Hkv, D, P):
+    """Slots of one page with gaps, in either direction, over the blocks' 32 tokens; skipped
+    tokens between pages.  Bounds start afresh with a page's first row, else go on."""
+    g = torch.Generator().manual_seed(D + P)
+    n_pages = 40
+    amax = torch.tensor([6.0, 6.0])
+    am = amax.cuda() if kind == "e4m3" else None
+    k = torch.zeros((n_pages, Hkv, P, D), dtype=pu.DTYPES[kind], device="cuda")
+    v, b = k.clone(), torch.zeros((n_pages, Hkv, 2, D), dtype=pu.DTYPES[kind], device="cuda")
+    shadow, want = [pu.values(k), pu.values(v)], pu.values(b)
+    for step in range(3):
+        slots = []
+        for p in torch.randperm(n_pages, generator=g).tolist():
+            rows = sorted(torch.randperm(P, generator=g)[:1 + int(torch.randint(P, (1,), generator=g))].tolist())
+            if step == 0 and 0 not in rows:
+                rows = [0] + rows
+            if p % 5 == 4:
+                rows.reverse()
+            slots += [p * P + i for i in rows]
+            slots += [-1] * (0 if p % 3 else int(torch.randint(1, 40, (1,), generator=g)))
+        rows = [torch.randn(len(slots), Hkv, D, generator=g).to(pu.rows_dtype(kind)) for _ in range(2)]
+        cp.cache_append_(rows[0].cuda(), rows[1].cuda(), torch.tensor(slots, device="cuda"), k, v, k_bounds=b, kv_amax=am)
+        assert cp.sync_status() == cp.OK
+        put = [pu.values(pu.stored(x, kind, 6.0)) if kind != "e4m3" else fp8.decode(pu.codes_of(x, 6.0)) for x in rows]
+        shadow = [paged.append(c, x, slots) for c, x in zip(shadow, put)]
+        for p in {s // P for s in slots if s >= 0}:
+            mine = [i for i, s in enumerate(slots) if s >= 0 and s // P == p]
+            lo, hi = put[0][mine].min(0), put[0][mine].max(0)
+            if not any(slots[i] % P == 0 for i in mine):
+                lo, hi = np.minimum(lo, want[p, :, 0]), np.maximum(hi, want[p, :, 1])
+            want[p, :, 0], want[p, :, 1] = lo, hi
+        assert np.array_equal(pu.values(k), shadow[0]) and np.array_equal(pu.values(v), shadow[1])
+        assert np.array_equal(pu.values(b), want)
