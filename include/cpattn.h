@@ -419,7 +419,9 @@ int cpattn_cache_append(const void* k_new, const void* v_new, long k_tok_stride,
  * cpattn_select_pages -- the pages that one new token per request attends to when
  * the context is too long to read whole.  For kv head h and page j
  *     score = max over the group's query heads i of sum_d max(q_id lo_d, q_id hi_d),
- * an upper bound of q.k over the page, summed in 64 bits and rounded to fp32.
+ * an upper bound of q.k over the page, summed in 64 bits and rounded to fp32.  Bounds
+ * may be infinite (a zero of q counts as zero beside them); a head whose sum is NaN does
+ * not count, and a page for which none counts ranks last.
  *   q              [R][Hq][D] dtype
  *   pages          [R][Hkv][budget] int32 (written): the `budget` pages with the
  *                  largest scores, ascending, ties to the lower page, -1 behind the

@@ -3,10 +3,12 @@
 // A page's score for kv head h is the largest q.k that any key inside the
 // page's bounds could have, over the query heads of the group:
 //     score = max_i sum_d max(q_id lo_d, q_id hi_d)
-//           = max_i sum_d (min(q_id, 0) lo_d + max(q_id, 0) hi_d)
+//           = max_i sum_d (min(q_id, 0) lo_d + max(q_id, 0) hi_d)      (lo <= hi, finite)
 // in 64 bits, rounded once to fp32: products of 16-bit values are exact there and
 // their sums almost always, so that the order of summation does not decide
-// between near pages.  The `budget` pages with the largest scores are listed in
+// between near pages.  Beside an infinite bound the second form would multiply it by
+// 0: there the first one is evaluated, with 0 for a zero of q (bound_term).  A head
+// whose sum is NaN does not count.  The `budget` pages with the largest scores are listed in
 // ascending order, ties to the lower page; the newest page and the first
 // keep_first pages are always among them.
 //
@@ -104,6 +106,11 @@ template <typename CT, int D>
 __device__ __forceinline__ const CT* bounds_of(const SelectArgs& a, const Pair& p, int page) {
   return static_cast<const CT*>(a.bounds) + ((size_t)page * a.Hkv + p.h) * 2 * D;
 }
+// max(q lo, q hi); NaN if a bound is
+__device__ __forceinline__ double bound_term(float q, float lo, float hi) {
+  if (lo != lo || hi != hi) return NAN;
+  return q == 0.f ? 0. : fmax((double)q * lo, (double)q * hi);
+}
 __device__ __forceinline__ bool in_pool(const SelectArgs& a, int page) { return (unsigned)page < (unsigned)a.num_pages; }
 
 // Scores of the block's pages in 64 bits on the tensor cores, 8 pages a warp.
@@ -145,12 +152,22 @@ struct Exact {
     }
   }
 
+  // One page's score for one head where the products gave NaN.
+  __device__ __noinline__ static float by_terms(const SelectArgs& a, const Pair& p, int page, int head) {
+    const CT* b = bounds_of<CT, D>(a, p, page);
+    const float* q = static_cast<const float*>(a.q) + ((size_t)p.r * a.Hq + (size_t)p.h * a.group + head) * D;
+    double sum = 0.;
+    for (int d = 0; d < D; ++d) sum += bound_term(q[d], b[d], b[D + d]);
+    return (float)sum;
+  }
+
   template <typename Put>
   __device__ __forceinline__ float score(const SelectArgs& a, const Pair& p, int h0, const char* s, Put put) {
     const double2(*s_q)[32] = reinterpret_cast<const double2(*)[32]>(s);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     for (int i0 = warp * 8; i0 < p.n; i0 += kWarps * 8) {
       const bool there = in_pool(a, page);
+      const int here = page;
       if (!there && t == 0) atomicOr(a.err, kErrPage);
       double acc[4][2] = {};
 #pragma unroll
@@ -181,8 +198,11 @@ struct Exact {
       uint32_t key = 0u;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const float x = (float)((acc[0][m] + acc[1][m]) + (acc[2][m] + acc[3][m]));
-        if (there && h0 + 2 * t + m < a.group) key = max(key, order_key(x));
+        float x = (float)((acc[0][m] + acc[1][m]) + (acc[2][m] + acc[3][m]));
+        if (there && h0 + 2 * t + m < a.group) {
+          if (x != x) x = by_terms(a, p, here, h0 + 2 * t + m);
+          key = max(key, order_key(x));
+        }
       }
       key = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
       key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
@@ -344,11 +364,7 @@ struct Approx {
     for (int m = h0; m < h1; ++m) {
       double sum = 0.;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float x = __bfloat162float(q[(size_t)m * D + e]);
-        sum = fma((double)fminf(x, 0.f), (double)lo[e], sum);
-        sum = fma((double)fmaxf(x, 0.f), (double)hi[e], sum);
-      }
+      for (int e = 0; e < V; ++e) sum += bound_term(__bfloat162float(q[(size_t)m * D + e]), lo[e], hi[e]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       key = max(key, order_key((float)sum));

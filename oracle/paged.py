@@ -76,18 +76,21 @@ def bounds(cache, table, lens):
 
 
 def scores(q, lo, hi):
-    """Upper bound of q.k over keys inside [lo, hi], the largest of the group's heads: q [group, D]."""
-    return max(float(np.sum(np.maximum(x * lo, x * hi))) for x in q)
+    """Upper bound of q.k over keys inside [lo, hi], the largest of the group's heads: q [group, D].
+    A zero of q counts as zero beside an infinite bound; heads whose sum is NaN do not count (NaN: none does)."""
+    with np.errstate(invalid="ignore"):
+        seen = ~(np.isnan(lo) | np.isnan(hi))
+        sums = [float(np.sum(np.where((x == 0) & seen, 0.0, np.maximum(x * lo, x * hi)))) for x in q]
+    return max([s for s in sums if s == s], default=float("nan"))
 
 
 def select(q, bounds_of, table, n, page_size, h, budget, keep_first):
     """Pages of one (request, kv head): q [group, D], bounds_of {(page, head): (lo, hi)}."""
     held = pages_of(n, page_size)
     s = [float(np.float32(scores(q, *bounds_of[int(table[j]), h]))) for j in range(held)]
-    for j in range(held):
-        if j < keep_first or j == held - 1:
-            s[j] = np.inf
-    best = sorted(range(held), key=lambda j: (-s[j], j))[:budget]
+    # the pages that are always listed, then by the score, NaN last
+    rank = lambda j: (not (j < keep_first or j == held - 1), s[j] != s[j], 0.0 if s[j] != s[j] else -s[j], j)
+    best = sorted(range(held), key=rank)[:budget]
     return sorted(best) + [-1] * (budget - len(best))
 
 

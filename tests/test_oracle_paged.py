@@ -70,3 +70,19 @@ def test_plan_refuses_a_length_above_its_table():
         out = paged.plan(lens, delta, table, ring, [0, 2], 16, 4)
         assert out[6] == paged.BAD_LENGTH and out[0] == lens and out[2] == ring and np.array_equal(out[1], table)
     assert paged.plan([32, 32], [0, -32], table, ring + [0] * 4, [0, 2], 16, 4)[6] == 0
+
+
+def test_scores_beside_infinite_and_nan_bounds():
+    inf, nan = np.inf, np.nan
+    lo, hi = np.array([-inf, -1.0, 0.5]), np.array([2.0, 1.0, 0.75])
+    assert paged.scores(np.array([[1.0, 1.0, 1.0]]), lo, hi) == 3.75
+    assert paged.scores(np.array([[0.0, 1.0, 1.0]]), lo, hi) == 1.75
+    assert paged.scores(np.array([[-1.0, 1.0, 1.0]]), lo, hi) == inf
+    bad = np.array([nan, 1.0, 1.0])
+    assert np.isnan(paged.scores(np.array([[0.0, 1.0, 1.0]]), lo, bad))
+    # a NaN page ranks behind one of -inf, and an infinite score does not take a forced page's place
+    bounds = {(0, 0): (np.array([-inf]), np.array([-inf])), (1, 0): (np.array([nan]), np.array([nan])),
+              (2, 0): (np.array([inf]), np.array([inf])), (3, 0): (np.array([0.0]), np.array([0.0]))}
+    one = np.array([[1.0]])
+    assert paged.select(one, bounds, [1, 0, 2, 3], 64, 16, 0, 3, 0) == [1, 2, 3]
+    assert paged.select(one, bounds, [2, 1, 0, 3], 64, 16, 0, 1, 0) == [3]

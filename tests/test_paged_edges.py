@@ -150,3 +150,34 @@ def test_append_bounds_of_pages_whose_new_tokens_leave_gaps(cp, kind, Hkv, D, P)
             want[p, :, 0], want[p, :, 1] = lo, hi
         assert np.array_equal(pu.values(k), shadow[0]) and np.array_equal(pu.values(v), shadow[1])
         assert np.array_equal(pu.values(b), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("pages,D,Hq,budget", [(90, 64, 2, 12), (300, 64, 2, 12), (700, 128, 9, 33)])
+def test_select_pages_with_infinite_bounds_by_the_definition(cp, kind, pages, D, Hq, budget):
+    """One infinite key leaves the other side of its column, and zeros of q leave the column out."""
+    g = torch.Generator().manual_seed(pages + D)
+    x = torch.randn(pages, 1, 2, D, generator=g).sort(2).values
+    inf = float("inf")
+    x[5, 0, 0, 3] = -inf
+    x[40, 0, 0, :5] = -inf
+    x[[5, 40], 0, 1] += 0.5
+    x[41, 0, 1, 7] = inf
+    x[41, 0, :, 11] = -inf
+    x[42, 0, :, 13] = torch.tensor([-inf, inf])
+    x[43, 0, 0, 20], x[43, 0, 1, 21] = -inf, inf
+    x[44, 0, 1, 30] = -inf
+    x[44, 0, 0, 30] = -inf
+    x[7, 0, :, 9] = float("nan")
+    b = x.to(pu.DTYPES[kind])
+    q = torch.randn(1, Hq, D, generator=g).abs().to(pu.rows_dtype(kind))
+    q[0, :, :12] = 0
+    q[0, 0, :4] = 1
+    q[0, 1, 20:22] *= -1
+    table = torch.randperm(pages, generator=g).int()[None]
+    n = 16 * pages - 1
+    got = cp.select_pages(q.cuda(), b.cuda(), table.cuda(), _i32([n]), 16, budget, keep_first=1)
+    assert cp.sync_status() == cp.OK
+    bv = pu.values(b)
+    exact = {(p, 0): (bv[p, 0, 0], bv[p, 0, 1]) for p in range(pages)}
+    assert got.cpu().tolist()[0][0] == paged.select(pu.values(q)[0], exact, table[0], n, 16, 0, budget, 1)
