@@ -407,7 +407,7 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
  *                  them: no token of another page and no skipped one between them
  *                  (their slots may leave gaps).  Bounds do not shrink when tokens are
  *                  taken back: they still cover the rows that were there.  NaN
- *                  keys are left out of them
+ *                  keys are left out of them; NaN where a column holds no others
  * A slot may appear once only.  N = 0 does nothing.
  */
 int cpattn_cache_append(const void* k_new, const void* v_new, long k_tok_stride, long k_head_stride,

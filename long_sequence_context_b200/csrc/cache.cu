@@ -428,6 +428,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
         for (int e = 0; e < P; ++e) lo[i * P + e] = fminf(lo[i * P + e], f[e]), hi[i * P + e] = fmaxf(hi[i * P + e], g[e]);
       }
     }
+    // a column of NaN keys alone has no bounds: NaN, which the next key's take the place of
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (lo[e] > hi[e]) lo[e] = hi[e] = NAN;
     // stored values: writing them again rounds nothing
     put<CT, V>(b, lo, 1.f);
     put<CT, V>(b + D, hi, 1.f);

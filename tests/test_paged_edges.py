@@ -181,3 +181,34 @@ def test_select_pages_with_infinite_bounds_by_the_definition(cp, kind, pages, D,
     bv = pu.values(b)
     exact = {(p, 0): (bv[p, 0, 0], bv[p, 0, 1]) for p in range(pages)}
     assert got.cpu().tolist()[0][0] == paged.select(pu.values(q)[0], exact, table[0], n, 16, 0, budget, 1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3"])
+def test_append_bounds_of_columns_that_hold_nan_keys(cp, kind):
+    """NaN keys are left out; where there is no other the bounds are NaN, and later keys replace them."""
+    Hkv, D, P, n_pages = 2, 64, 16, 40
+    am = torch.tensor([448.0, 448.0], device="cuda") if kind == "e4m3" else None
+    k = torch.zeros((n_pages, Hkv, P, D), dtype=pu.DTYPES[kind], device="cuda")
+    v, b = k.clone(), torch.zeros((n_pages, Hkv, 2, D), dtype=pu.DTYPES[kind], device="cuda")
+    g = torch.Generator().manual_seed(19)
+    x = torch.randint(-6, 7, (n_pages * P, Hkv, D), generator=g).to(pu.rows_dtype(kind))  # exact in 8 bits
+    x[3 * P:3 * P + 9, 1, 5] = float("nan")
+    x[7 * P + 2, 0, 50] = float("nan")
+    some = torch.arange(n_pages * P).view(n_pages, P)
+    first, second = some[:, :9].reshape(-1), some[:, 9:].reshape(-1)
+    def bounds(y):  # numpy's fmin and fmax leave NaN out, and give it where there is nothing else
+        y = y.float().numpy().reshape(n_pages, -1, Hkv, D)
+        return np.stack([np.fmin.reduce(y, 1), np.fmax.reduce(y, 1)], 2)
+    for part, upto in ((first, bounds(x[first])), (second, bounds(x))):
+        cp.cache_append_(x[part].cuda(), x[part].cuda(), part.cuda(), k, v, k_bounds=b, kv_amax=am)
+        assert cp.sync_status() == cp.OK
+        assert np.array_equal(pu.values(b), upto, equal_nan=True)
+        assert np.isnan(upto).sum() == (2 if part is first else 0)
+        # a page whose bounds are NaN ranks last, whatever the other columns say
+        q = torch.full((1, Hkv, D), 40.0).to(x.dtype)
+        table = torch.arange(n_pages, dtype=torch.int32)[None].cuda()
+        got = cp.select_pages(q.cuda(), b, table, _i32([n_pages * P]), P, n_pages - 1).cpu().tolist()[0]
+        bv, qv = pu.values(b), pu.values(q)[0]
+        exact = {(p, h): (bv[p, h, 0], bv[p, h, 1]) for p in range(n_pages) for h in range(Hkv)}
+        assert got == [paged.select(qv[h:h + 1], exact, range(n_pages), n_pages * P, P, h, n_pages - 1, 0) for h in range(Hkv)]
+        assert part is second or 3 not in got[1]
