@@ -14,10 +14,10 @@
 //
 // Scoring every page in 64 bits is what that would cost most (64 products a cycle
 // and SM).  For 16- and 8-bit bounds the tensor cores score in fp32 first, with an
-// error below eps = 2D 2^-23 sum |q| max |bound| (2D additions of at most two units
-// in the last place each): of a page more than 2 eps above or below the budget-th
-// largest score it is then known on which side it stands, and only those between,
-// a few, are scored in 64 bits.
+// error below some eps (derived where it is computed).  The budget-th largest of these
+// scores is then within eps of the exact one: of a page more than 2 eps above or below
+// it is known on which side it stands, and only those between, a few, are scored in
+// 64 bits.
 //
 // One cluster of thread blocks takes one (request, kv head): every block scores
 // a stretch of pages and sends the scores to the first block's shared memory,
@@ -568,8 +568,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       for (int i = 0; i < 8; ++i) norm = fmaxf(norm, s_norm[i]);
       for (int i = 0; i < ranks; ++i) most = fmaxf(most, s_most[i]);
       const float at = key_value(threshold);
-      // the last term: products and operands below the normal range
-      const float eps = norm * most * ((D / 2 + 2) * 0x1p-23f) * 1.01f + fabsf(at) * 0x1p-22f +
+      // The error of a score in fp32.  Each of the four accumulators takes D / 2 products, exact
+      // before they are added, by D / 32 instructions of 16.  Whatever order an instruction adds
+      // its 17 numbers in, rounding or cutting off each sum to fp32, or cutting all of them off
+      // at the largest one's last place: it loses at most 17 units of 2^-23 S_i, S_i the sum of
+      // the accumulator's |terms|.  The three sums of the accumulators lose less than 2 2^-23
+      // sum S_i, and sum S_i <= sum |q| max |bound|, whose own rounding the 1.01 covers.  Then the
+      // rounding of the exact score, and products and operands below the normal range.  (A band
+      // twice as wide: 2048 pages 10.8 us for 10.0.)
+      const float eps = norm * most * ((17 * D / 32 + 3) * 0x1p-23f) * 1.01f + fabsf(at) * 0x1p-22f +
                         2 * D * 0x1p-126f * (norm + most + 1.f);
       uint32_t low = 0u, high = kAlways - 1u;
       if (threshold != 0u && eps < 1e37f && fabsf(at) < 1e37f)

@@ -212,3 +212,27 @@ def test_append_bounds_of_columns_that_hold_nan_keys(cp, kind):
         exact = {(p, h): (bv[p, h, 0], bv[p, h, 1]) for p in range(n_pages) for h in range(Hkv)}
         assert got == [paged.select(qv[h:h + 1], exact, range(n_pages), n_pages * P, P, h, n_pages - 1, 0) for h in range(Hkv)]
         assert part is second or 3 not in got[1]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,Hq,pages,budget", [(128, 1, 3000, 700), (64, 5, 400, 150)])
+def test_select_sums_that_cancel(cp, kind, D, Hq, pages, budget):
+    """Terms of hundreds whose sums differ by less than fp32 sums are off: the band around the
+    threshold has to hold every page that could be on either side."""
+    g = torch.Generator().manual_seed(pages)
+    half = torch.randint(64, 449, (pages, 1, 1, D // 2), generator=g).float()
+    half = half.to(torch.float8_e4m3fn).float()
+    x = torch.cat([half, -half], 3)[..., torch.randperm(D, generator=g)]
+    few = torch.randint(D, (pages,), generator=g)
+    x[torch.arange(pages), 0, 0, few] *= 1 + torch.randint(0, 2, (pages,), generator=g) / 8
+    b = x.expand(pages, 1, 2, D).contiguous()
+    b = b.to(torch.float8_e4m3fn).view(torch.uint8) if kind == "e4m3" else b.bfloat16()
+    q = (1 + torch.randint(0, 128, (1, Hq, D), generator=g) / 128).bfloat16()
+    q[..., ::3] = 1 + 2.0 ** -7
+    table = torch.randperm(pages, generator=g).int()[None]
+    n = 16 * pages - 5
+    got = cp.select_pages(q.cuda(), b.cuda(), table.cuda(), _i32([n]), 16, budget)
+    assert cp.sync_status() == cp.OK
+    bv = pu.values(b)
+    exact = {(p, 0): (bv[p, 0, 0], bv[p, 0, 1]) for p in range(pages)}
+    assert got.cpu().tolist()[0][0] == paged.select(pu.values(q)[0], exact, table[0], n, 16, 0, budget, 0)
