@@ -7,15 +7,18 @@ Each csrc/*.cu is compiled by nvcc (-gencode arch=compute_100a,code=sm_100a
 -O3 -lineinfo) into _build/, then linked into long_sequence_context_b200/
 libcpattn.so with the CUDA runtime linked statically.  No vendor math library
 is linked: every kernel is this package's own.  csrc/calls.cpp is host code
-against PyTorch's headers, compiled by g++.
+against PyTorch's headers, compiled by g++ for the torch and Python that are
+installed; where that fails the binding does without it.
 """
 import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -56,20 +59,48 @@ def _compile(src, verbose):
     return obj, (r.stdout + r.stderr)
 
 
+def _torch():
+    """torch's folder and version, without importing it."""
+    path = importlib.util.find_spec("torch").submodule_search_locations[0]
+    with open(os.path.join(path, "version.py")) as f:
+        return path, re.search(r"^__version__ = ['\"](.*)['\"]", f.read(), re.M).group(1)
+
+
+def calls_tag(torch_version):
+    """What a _calls.so is built for: it uses the C++ interfaces of one torch and the C API of one Python."""
+    return f"torch {torch_version}, python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
 def _build_calls(force):
-    src = os.path.join(CSRC, "calls.cpp")
-    if not (force or _stale(CALLS, [src, os.path.join(ROOT, "include", "cpattn.h")])):
+    src, stamp = os.path.join(CSRC, "calls.cpp"), os.path.join(BUILD, "calls.tag")
+    torch_dir, version = _torch()
+    tag, old = calls_tag(version), None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            old = f.read()
+    if not (force or old != tag or _stale(CALLS, [src, os.path.join(ROOT, "include", "cpattn.h")])):
         return
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
            "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(cuda, "include"),
-           "-I", sysconfig.get_paths()["include"], src, "-o", CALLS + ".tmp", "-L", os.path.join(torch_dir, "lib"),
+           "-I", sysconfig.get_paths()["include"], f'-DCALLS_TAG="{tag}"', src, "-o", CALLS + ".tmp",
+           "-L", os.path.join(torch_dir, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(CALLS + ".tmp", CALLS)
+    with open(stamp, "w") as f:
+        f.write(tag)
+
+
+def _try_calls(force):
+    try:
+        _build_calls(force)
+    except (RuntimeError, OSError, AttributeError) as e:  # no compiler, no headers, another torch's headers
+        if os.path.exists(CALLS):  # of other sources
+            os.remove(CALLS)
+        warnings.warn(f"_calls.so was not built, the paged cache's calls go through ctypes: {e}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -91,7 +122,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    _build_calls(force)
+    _try_calls(force)
     if verbose:
         print("\n".join(logs))
     return LIB

@@ -8,8 +8,11 @@ library has not been built, importing this module raises.
 """
 import ctypes
 import os
+import warnings
 
 import torch
+
+from long_sequence_context_b200.build import calls_tag
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcpattn.so")
@@ -91,12 +94,26 @@ def _load():
 lib = _load()
 
 
+class _NoCalls:
+    """In the place of _calls.so: declines every call, which then goes through ctypes."""
+
+    def cache_plan(*args):
+        return None
+
+    cache_append = select_pages = decode = cache_plan
+
+
 def _load_calls():
+    # only a shortcut: nothing is lost without it but some microseconds of a paged cache's calls
     try:
         from long_sequence_context_b200 import _calls
-    except ImportError as e:
-        raise ImportError("_calls.so is missing or does not load: build it with "
-                          "`python -m long_sequence_context_b200.build`") from e
+        why = None if _calls.tag == calls_tag(torch.__version__) else f"built for {_calls.tag}"
+    except (ImportError, AttributeError) as e:
+        why = str(e)
+    if why is not None:
+        warnings.warn(f"_calls.so is not used ({why}); the paged cache's calls go through ctypes. "
+                      "Build it with `python -m long_sequence_context_b200.build`")
+        return _NoCalls()
     _calls.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                   for n in ("cpattn_cache_plan_workspace_bytes", "cpattn_cache_plan", "cpattn_cache_append",
                             "cpattn_select_pages", "cpattn_decode_workspace_bytes", "cpattn_decode")))

@@ -9,7 +9,8 @@
 // argument that is wrong, and its ctypes calls, which take the rarer ones
 // (outputs, workspaces and streams given).  Otherwise it returns the C
 // function's status and the outputs.  The library's functions come as addresses
-// (bind), so that both ways call the same loaded library.
+// (bind), so that both ways call the same loaded library.  cpattn.py does without
+// this module where it is missing or was built for another torch or Python (tag).
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
@@ -259,4 +260,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "tag", CALLS_TAG) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
