@@ -570,6 +570,15 @@ def _here(t, name: str, dev: int):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _ints(**sizes):
+    """Whole numbers that the C ABI takes as int: ctypes would pass on the low bits of a larger one."""
+    for name, x in sizes.items():
+        if not isinstance(x, int):
+            raise TypeError(f"{name} must be an int, got {type(x).__name__}")
+        if not -(1 << 31) <= x < 1 << 31:
+            raise ValueError(f"{name} is out of range: {x}")
+
+
 def _scratch(workspace, need, like):
     workspace = _workspace(workspace, need, like)
     if not workspace.is_contiguous():
@@ -582,6 +591,7 @@ def _p(t):
 
 
 def cache_plan_workspace_bytes(R, capacity) -> int:
+    _ints(R=R, capacity=capacity)
     return int(lib.cpattn_cache_plan_workspace_bytes(R, capacity))
 
 
@@ -611,6 +621,7 @@ def cache_plan(lens, delta, block_table, free_ring, free_state, page_size: int, 
     _expect(free_ring, "free_ring", free_ring.shape, torch.int32, block_table)
     _expect(free_state, "free_state", (2,), torch.int32, block_table)
     num_pages, dev = free_ring.shape[0], block_table.get_device()
+    _ints(R=R, max_pages=max_pages, num_pages=num_pages, page_size=page_size, capacity=capacity)
     if lens_out is not None:
         _expect(lens_out, "lens_out", (R,), torch.int32, block_table)
     if free_state_out is not None:
@@ -664,6 +675,7 @@ def cache_append_(k_new, v_new, slots, k_cache, v_cache, k_bounds=None, kv_amax=
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a [N] tensor")
     N = slots.shape[0]
+    _ints(num_pages=num_pages, kv_heads=heads, page_size=page_size)
     _expect(slots, "slots", (N,), torch.int64, k_cache)
     ks = _rows(k_new, "k_new", (N, heads, D), dtype, k_cache)
     vs = _rows(v_new, "v_new", (N, heads, D), dtype, k_cache)
@@ -698,6 +710,7 @@ def select_pages(q, k_bounds, block_table, lens, page_size: int, budget: int, ke
         raise ValueError(f"k_bounds is empty: {tuple(k_bounds.shape)}")
     _expect(k_bounds, "k_bounds", (num_pages, heads, 2, D), k_bounds.dtype)
     R, Hq, max_pages = _queries(q, block_table, lens, dtype, heads, D, k_bounds)
+    _ints(R=R, Hq=Hq, max_pages=max_pages, num_pages=num_pages, page_size=page_size, budget=budget, keep_first=keep_first)
     if budget < 1 or keep_first < 0 or budget <= keep_first:
         raise ValueError(f"budget ({budget}) must be above keep_first ({keep_first}), and keep_first not negative")
     s = _here(q, "q", dev)
@@ -709,6 +722,7 @@ def select_pages(q, k_bounds, block_table, lens, page_size: int, budget: int, ke
 
 
 def decode_workspace_bytes(R, Hq, Hkv, D) -> int:
+    _ints(R=R, Hq=Hq, Hkv=Hkv, D=D)
     return int(lib.cpattn_decode_workspace_bytes(R, Hq, Hkv, D))
 
 
@@ -734,6 +748,7 @@ def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, sca
             raise ValueError("pages must be a [R, kv_heads, budget] tensor")
         budget = pages.shape[2]
         _expect(pages, "pages", (R, heads, budget), torch.int32, k_cache)
+    _ints(R=R, Hq=Hq, max_pages=max_pages, num_pages=num_pages, page_size=page_size, budget=budget)
     out_dtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
     if out_dtype != torch.bfloat16 and out_dtype != torch.float32:
         raise TypeError(f"unsupported dtype {out_dtype}")
