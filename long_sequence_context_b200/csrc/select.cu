@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   }
   const int held = (int)((len + (1 << a.shift) - 1) >> a.shift);
   if (held <= a.budget) {  // everything is selected (the whole cluster leaves here)
-    for (int j = rank * kThreads + tid; j < a.budget; j += ranks * kThreads) out[j] = j < held ? j : -1;
+    // unsigned: a step past a budget near 2^31 is no int
+    for (unsigned j = rank * kThreads + tid; j < (unsigned)a.budget; j += ranks * kThreads) out[j] = (int)j < held ? (int)j : -1;
     __syncwarp();
     cluster.barrier_wait();
     return;

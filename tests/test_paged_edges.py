@@ -236,3 +236,15 @@ def test_select_sums_that_cancel(cp, kind, D, Hq, pages, budget):
     bv = pu.values(b)
     exact = {(p, 0): (bv[p, 0, 0], bv[p, 0, 1]) for p in range(pages)}
     assert got.cpu().tolist()[0][0] == paged.select(pu.values(q)[0], exact, table[0], n, 16, 0, budget, 0)
+
+
+@pytest.mark.parametrize("width", [3, 5000])
+def test_select_largest_budget(cp, width):
+    """2^31 - 1 entries (8.6 GB), of which a request of three pages fills three."""
+    q, b = torch.zeros((1, 1, 64), device="cuda"), torch.zeros((3, 1, 2, 64), device="cuda")
+    table = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    table[0, :3] = torch.arange(3)
+    got = cp.select_pages(q, b, table, _i32([40]), 16, 2 ** 31 - 1, keep_first=7)[0, 0]
+    assert cp.sync_status() == cp.OK
+    assert got[:3].tolist() == [0, 1, 2]
+    assert got[3:].max().item() == got[3:].min().item() == -1
