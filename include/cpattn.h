@@ -385,7 +385,8 @@ enum {
  * returned is recorded (CPATTN_ERR_PAGE) and passed on, and its tokens get slot -1.
  * Workspace: cpattn_cache_plan_workspace_bytes(R, capacity), 16-byte aligned;
  * contents on entry are ignored; calls that can overlap on the GPU need one each.
- * 0 (and NULL) for steps of up to 1024 requests and 2048 tokens.
+ * 0 (and NULL) for steps of up to 1024 requests and 2048 tokens.  At most 2^30
+ * requests (CPATTN_ERR_SHAPE).
  */
 size_t cpattn_cache_plan_workspace_bytes(int R, long capacity);
 int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_table, int R,

@@ -476,6 +476,7 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   NvtxRange nv("cpattn_cache_plan");
   const int shift = paged::page_shift(page_size);
   if (R < 1 || max_pages < 1 || num_pages < 1 || shift < 0) return CPATTN_ERR_SHAPE;
+  if (R > 1 << 30) return CPATTN_ERR_SHAPE;  // find() adds two request numbers
   if (capacity < 0 || capacity > 0x7fffffffL) return CPATTN_ERR_SHAPE;
   if (((long long)max_pages << shift) > 0x7fffffffLL) return CPATTN_ERR_SHAPE;
   if (!lens || !delta || !block_table || !free_ring || !free_state || !lens_out || !free_state_out || !cu_new ||

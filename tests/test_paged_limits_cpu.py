@@ -1,0 +1,19 @@
+"""Sizes that the kernels' 32-bit counters do not hold are refused by the C ABI, on the CPU."""
+import ctypes
+
+import pytest
+
+from long_sequence_context_b200 import cpattn as cp
+from tests.test_paged_cpu import VP, _c_decode
+
+
+def _plan(R):
+    return cp.lib.cpattn_cache_plan(VP, VP, VP, R, 1, 16, VP, VP, 16, VP, VP, VP, VP, 4, VP, VP, 1 << 40, None)
+
+
+def test_plan_requests():
+    """Its search halves sums of two request numbers: up to 2^30 requests."""
+    n0 = cp.launch_count()
+    for R in ((1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1):
+        assert _plan(R) == cp.ERR_SHAPE
+    assert cp.launch_count() == n0
