@@ -409,7 +409,8 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
  *                  (their slots may leave gaps).  Bounds do not shrink when tokens are
  *                  taken back: they still cover the rows that were there.  NaN
  *                  keys are left out of them; NaN where a column holds no others
- * A slot may appear once only.  N = 0 does nothing.
+ * A slot may appear once only.  N = 0 does nothing.  At most 2^25 kv heads and 2^34
+ * rows, N * Hkv (CPATTN_ERR_SHAPE).
  */
 int cpattn_cache_append(const void* k_new, const void* v_new, long k_tok_stride, long k_head_stride,
                         long v_tok_stride, long v_head_stride, const int64_t* slots, long N,

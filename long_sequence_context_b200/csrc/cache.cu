@@ -554,6 +554,7 @@ int cpattn_cache_append(const void* k_new, const void* v_new, long k_tok_stride,
   const int shift = paged::page_shift(page_size);
   if (N < 0 || Hkv < 1 || (D != 64 && D != 128) || shift < 0 || num_pages < 1) return CPATTN_ERR_SHAPE;
   if (N > 0x7fffffffL || (long long)N * Hkv > (1LL << 34)) return CPATTN_ERR_SHAPE;
+  if (Hkv > 1 << 25) return CPATTN_ERR_SHAPE;  // a block counts 32 stretches of so many heads
   // the stride of an axis of one says nothing
   if (N <= 1) k_tok_stride = v_tok_stride = 0;
   if (Hkv == 1) k_head_stride = v_head_stride = 0;

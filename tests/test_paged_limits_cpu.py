@@ -17,3 +17,12 @@ def test_plan_requests():
     for R in ((1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1):
         assert _plan(R) == cp.ERR_SHAPE
     assert cp.launch_count() == n0
+
+
+def test_append_heads():
+    """A block counts the heads of up to 32 stretches of tokens as an int: up to 2^25 heads."""
+    n0 = cp.launch_count()
+    for heads in ((1 << 25) + 1, 1 << 26, (1 << 31) - 1):
+        st = cp.lib.cpattn_cache_append(VP, VP, 64, 64, 64, 64, VP, 4, VP, VP, None, heads, 64, 16, 1, None, 0, 0, None)
+        assert st == cp.ERR_SHAPE
+    assert cp.launch_count() == n0
