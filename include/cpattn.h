@@ -455,8 +455,8 @@ int cpattn_select_pages(const void* q, const void* k_bounds, const int32_t* bloc
  * Workspace: cpattn_decode_workspace_bytes(R, Hq, Hkv, D) (0 for invalid sizes),
  * 256-byte aligned; contents on entry are ignored; calls that can overlap on the
  * GPU need one each.  Results do not depend on it, nor on other requests' values.
- * Limits (CPATTN_ERR_SHAPE): a cache below 256 GB each for K and V, and R * Hkv *
- * (tokens of a table's row / 64 + 4) < 2^31.
+ * Limits (CPATTN_ERR_SHAPE): a cache below 256 GB each for K and V, Hq * D <= 2^30, and
+ * R * Hkv * (tokens of a table's row / 64 + 4) < 2^31.
  */
 size_t cpattn_decode_workspace_bytes(int R, int Hq, int Hkv, int D);
 int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,

@@ -1095,6 +1095,7 @@ int cpattn_decode(const void* q, const void* k_cache, const void* v_cache,
   if (!sizes_ok(R, Hq, Hkv, D) || shift < 0 || max_pages < 1 || num_pages < 1) return CPATTN_ERR_SHAPE;
   if (((long long)max_pages << shift) > 0x7fffffffLL) return CPATTN_ERR_SHAPE;
   if ((long long)R * Hq * D > (1LL << 40)) return CPATTN_ERR_SHAPE;
+  if ((long long)Hq * D > (1LL << 30)) return CPATTN_ERR_SHAPE;  // a block counts a request's outputs in 31 bits
   // the kernel counts the cache's lines of 128 bytes in 31 bits (256 GB)
   const long long row_bytes = (long long)D * (cache_dtype == CPATTN_FP32 ? 4 : cache_dtype == CPATTN_BF16 ? 2 : 1);
   if ((long long)num_pages * Hkv > (1LL << 38) / row_bytes >> shift) return CPATTN_ERR_SHAPE;

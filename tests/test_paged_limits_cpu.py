@@ -1,6 +1,4 @@
 """Sizes that the kernels' 32-bit counters do not hold are refused by the C ABI, on the CPU."""
-import ctypes
-
 import pytest
 
 from long_sequence_context_b200 import cpattn as cp
@@ -25,4 +23,12 @@ def test_append_heads():
     for heads in ((1 << 25) + 1, 1 << 26, (1 << 31) - 1):
         st = cp.lib.cpattn_cache_append(VP, VP, 64, 64, 64, 64, VP, 4, VP, VP, None, heads, 64, 16, 1, None, 0, 0, None)
         assert st == cp.ERR_SHAPE
+    assert cp.launch_count() == n0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [((1 << 23) + 64, (1 << 17) + 1, 128), (1 << 25, 1 << 19, 64), (1 << 26, 1 << 26, 128)])
+def test_decode_outputs_of_a_request(Hq, Hkv, D):
+    """The outputs of a request without a key are counted as an int: Hq * D up to 2^30."""
+    n0 = cp.launch_count()
+    assert _c_decode(R=1, Hq=Hq, Hkv=Hkv, D=D, width=1, pages=1) == cp.ERR_SHAPE
     assert cp.launch_count() == n0
