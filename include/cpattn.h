@@ -373,7 +373,8 @@ enum {
  *   lens_out       [R], free_state_out [2]: the new lengths and state (written);
  *                  may be the same memory as lens and free_state.  With other
  *                  memory the call can be repeated and gives the same again, and
- *                  larger steps are faster.  No other output may overlap an input
+ *                  larger steps are faster.  Nothing else that is written may overlap
+ *                  anything that is read or written (CPATTN_ERR_ARG)
  *   block_table, free_ring: entries of pages taken and returned are written, the
  *                  others (those of returned pages too) left as they are
  *   cu_new         [R + 1]: first new token of request r in the packed order

@@ -259,7 +259,14 @@ __global__ void __launch_bounds__(256) plan_items_kernel(const PlanArgs a) {
   plan_items(a, p, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
 }
 
-bool overlap(const int32_t* x, const int32_t* y, long n) { return x < y + n && y < x + n; }
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return a < b + y.bytes && b < a + x.bytes;
+}
 
 struct AppendArgs {
   const void *k, *v;
@@ -490,6 +497,19 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   const size_t need = cpattn_cache_plan_workspace_bytes(R, capacity);
   if (need && (!workspace || ws_bytes < need)) return CPATTN_ERR_WORKSPACE;
   if (!paged::aligned_to(workspace, 16)) return CPATTN_ERR_ALIGN;
+  // Blocks read what others have not written yet: nothing that is written may lie in anything
+  // else, but the lengths and the state in their own place.
+  const size_t requests = (size_t)R * sizeof(int32_t);
+  const Span written[] = {{lens_out, requests}, {free_state_out, 8}, {block_table, requests * max_pages},
+                          {free_ring, (size_t)num_pages * 4}, {cu_new, requests + 4}, {slots, (size_t)capacity * 8},
+                          {verdict, 4}, {workspace, need}};
+  const Span read[] = {{lens, requests}, {free_state, 8}, {delta, requests}};
+  for (int i = 0; i < 8; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i], written[j])) return CPATTN_ERR_ARG;
+    for (int j = 0; j < 3; ++j)
+      if (overlap(written[i], read[j]) && !(i == j && j < 2 && written[i].p == read[j].p)) return CPATTN_ERR_ARG;
+  }
   unsigned* err = device_error_word();
   if (!err) return CPATTN_ERR_CUDA;
   PlanArgs a = {};
@@ -520,7 +540,7 @@ int cpattn_cache_plan(const int32_t* lens, const int32_t* delta, int32_t* block_
   const long long items = std::max<long long>(capacity, std::min<long long>((long long)R * max_pages, num_pages));
   const unsigned blocks =
       (unsigned)std::max<long long>(1, std::min<long long>((items + 255) / 256, (long long)num_sms(dev) * 2));
-  const bool in_place = overlap(lens, lens_out, R) || overlap(free_state, free_state_out, 2);
+  const bool in_place = lens == lens_out || free_state == free_state_out;
   const bool many = R <= kSmallR && !in_place;
   if (many || !need) {
     // fewer warps' sums to add in a small block: 16 requests 3.0 us with 256 threads, 5.1 with 1024
