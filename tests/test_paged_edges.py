@@ -248,3 +248,35 @@ def test_select_largest_budget(cp, width):
     assert cp.sync_status() == cp.OK
     assert got[:3].tolist() == [0, 1, 2]
     assert got[3:].max().item() == got[3:].min().item() == -1
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp32"])
+@pytest.mark.parametrize("R,Hkv,Hq,D,width,budget", [(1, 1, 2, 64, 49152, 700), (1, 2, 18, 128, 24577, 15423),
+                                                     (1, 1, 1, 64, 24576, 300), (40, 4, 4, 64, 9000, 200)])
+def test_select_over_the_widest_tables(cp, kind, R, Hkv, Hq, D, width, budget):
+    """Scores of up to 192 KB of a block's shared memory, with clusters of every size; near the
+    threshold many pages of alike bounds."""
+    g = torch.Generator().manual_seed(width + Hq)
+    pool = min(R * width, 60000)
+    x = torch.randn(pool, Hkv, 2, D, generator=g).sort(2).values
+    x[1::2] = x[::2][:pool // 2]  # pairs of equal pages
+    b = x.to(torch.float8_e4m3fn).view(torch.uint8) if kind == "e4m3" else x.to(pu.DTYPES[kind])
+    q = torch.randn(R, Hq, D, generator=g).to(pu.rows_dtype(kind))
+    table = torch.stack([torch.randperm(pool, generator=g)[:width] for _ in range(R)]).int()
+    held = [width - (r * 311) % width for r in range(R)]
+    lens = [16 * n - r % 16 for r, n in enumerate(held)]
+    got = cp.select_pages(q.cuda(), b.cuda(), table.cuda(), _i32(lens), 16, budget, keep_first=2).cpu()
+    assert cp.sync_status() == cp.OK
+    bv, qv, group = pu.values(b), pu.values(q), Hq // Hkv
+    lo, hi = (torch.from_numpy(bv[:, :, i]).cuda() for i in (0, 1))
+    for r in range(R):
+        ids = table[r, :held[r]].long().cuda()
+        for h in range(Hkv):
+            # the definition in 64 bits, a head at a time
+            s = torch.stack([torch.maximum(x * lo[ids, h], x * hi[ids, h]).sum(1)
+                             for x in torch.from_numpy(qv[r, h * group:(h + 1) * group]).cuda()]).amax(0).float()
+            s[:2] = float("inf")
+            s[-1] = float("inf")
+            n = min(budget, held[r])
+            want = s.sort(descending=True, stable=True).indices[:n].sort().values.int().cpu()
+            assert torch.equal(got[r, h, :n], want) and torch.all(got[r, h, n:] == -1), (r, h)
