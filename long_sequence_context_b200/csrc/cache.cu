@@ -279,15 +279,11 @@ struct AppendArgs {
   int Hkv, shift;
 };
 
-// Words of V elements of type T in place; V * sizeof(T) is 8 or 16 bytes.
-template <int B>
-__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[B / 4]) {
-  if constexpr (B == 16)
-    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(p));
-  else
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+// 16 bytes, in place
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[4]) {
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
 }
 
 // V floats as stored; f becomes the numbers that are then stored (unscaled).
@@ -383,8 +379,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
         for (int x = 0; x < kAhead; ++x) {
           const int i = i0 + x * kRows;
           if (i < len) {
-            load_words<16>(k + i * a.k_tok, kw[x]);
-            load_words<16>(v + i * a.v_tok, vw[x]);
+            load_words(k + i * a.k_tok, kw[x]);
+            load_words(v + i * a.v_tok, vw[x]);
           }
         }
 #pragma unroll

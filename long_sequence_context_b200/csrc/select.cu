@@ -53,7 +53,7 @@ struct SelectArgs {
   const int32_t *table, *lens;
   int32_t* sel;
   unsigned* err;
-  int R, Hq, Hkv, group, shift, max_pages, num_pages, budget, keep_first, q_bf16;
+  int R, Hq, Hkv, group, shift, max_pages, num_pages, budget, keep_first;
 };
 
 // unsigned order of the keys = order of the scores; NaN is below every number
@@ -68,18 +68,14 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// W consecutive words, in place.
+// W (a multiple of 4) consecutive words, in place.
 template <int W>
 __device__ __forceinline__ void load_packed(const void* p, uint32_t (&w)[W]) {
-  if constexpr (W < 4) {
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  } else {
 #pragma unroll
-    for (int i = 0; i < W; i += 4)
-      asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "l"(static_cast<const char*>(p) + 4 * i));
-  }
+  for (int i = 0; i < W; i += 4)
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                 : "l"(static_cast<const char*>(p) + 4 * i));
 }
 
 // c (8 pages x 8 heads, 64 bits) += a (8 pages x 4 columns) b (4 columns x 8 heads)
@@ -113,21 +109,20 @@ __device__ __forceinline__ double bound_term(float q, float lo, float hi) {
 }
 __device__ __forceinline__ bool in_pool(const SelectArgs& a, int page) { return (unsigned)page < (unsigned)a.num_pages; }
 
-// Scores of the block's pages in 64 bits on the tensor cores, 8 pages a warp.
-template <typename CT, int D>
+// Scores of the block's pages in 64 bits on the tensor cores, 8 pages a warp: fp32 bounds.
+template <int D>
 struct Exact {
-  // A warp takes 8 pages at a time, 4 lanes each, in steps of W words (E columns) of
-  // a lane's low and high bounds.
-  static constexpr int P = Unpack<CT>::kPerWord;
-  static constexpr int W = D / (4 * P) < 8 ? D / (4 * P) : 8, E = W * P, STEPS = D / (4 * E);
+  // A warp takes 8 pages at a time, 4 lanes each, in steps of E columns of a lane's low
+  // and high bounds.
+  static constexpr int E = 8, STEPS = D / (4 * E);
   static constexpr int kQueryBytes = STEPS * E * 32 * 16;
 
-  uint32_t lo[W], hi[W];
+  uint32_t lo[E], hi[E];
   int page, page_next;
 
   __device__ __forceinline__ int page_of(const Pair& p, int i) const { return p.table[p.first + min(i, p.n - 1)]; }
   __device__ __forceinline__ void load(const SelectArgs& a, const Pair& p, int step) {
-    const CT* b = bounds_of<CT, D>(a, p, in_pool(a, page) ? page : 0) + step * 4 * E + (threadIdx.x & 3) * E;
+    const float* b = bounds_of<float, D>(a, p, in_pool(a, page) ? page : 0) + step * 4 * E + (threadIdx.x & 3) * E;
     load_packed(b, lo);
     load_packed(b + D, hi);
   }
@@ -154,7 +149,7 @@ struct Exact {
 
   // One page's score for one head where the products gave NaN.
   __device__ __noinline__ static float by_terms(const SelectArgs& a, const Pair& p, int page, int head) {
-    const CT* b = bounds_of<CT, D>(a, p, page);
+    const float* b = bounds_of<float, D>(a, p, page);
     const float* q = static_cast<const float*>(a.q) + ((size_t)p.r * a.Hq + (size_t)p.h * a.group + head) * D;
     double sum = 0.;
     for (int d = 0; d < D; ++d) sum += bound_term(q[d], b[d], b[D + d]);
@@ -174,10 +169,7 @@ struct Exact {
       for (int step = 0; step < STEPS; ++step) {
         float flo[E], fhi[E];
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          Unpack<CT>::word(lo[w], flo + w * P);
-          Unpack<CT>::word(hi[w], fhi + w * P);
-        }
+        for (int e = 0; e < E; ++e) flo[e] = __uint_as_float(lo[e]), fhi[e] = __uint_as_float(hi[e]);
         if (step + 1 < STEPS) {
           load(a, p, step + 1);
         } else {
@@ -474,7 +466,7 @@ __device__ __noinline__ void find_threshold(const uint32_t* keys, int n, int bud
 template <typename CT, int D>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   constexpr bool kApprox = sizeof(CT) < 4;
-  using Scores = std::conditional_t<kApprox, Approx<CT, D>, Exact<CT, D>>;
+  using Scores = std::conditional_t<kApprox, Approx<CT, D>, Exact<D>>;
   extern __shared__ __align__(16) uint32_t s_key[];  // the first block's: the keys of all pages
   __shared__ __align__(16) char s_q[Scores::kQueryBytes];
   __shared__ Search s_search;
@@ -729,7 +721,6 @@ extern "C" int cpattn_select_pages(const void* q, const void* k_bounds, const in
   a.num_pages = num_pages;
   a.budget = budget;
   a.keep_first = keep_first;
-  a.q_bf16 = dtype == CPATTN_BF16;
   int dev = 0;
   cudaGetDevice(&dev);
   // Blocks per pair: while there are at most four to an SM, and a block still has 64
