@@ -748,6 +748,8 @@ def decode(q, k_cache, v_cache, block_table, lens, pages=None, kv_amax=None, sca
             raise ValueError("pages must be a [R, kv_heads, budget] tensor")
         budget = pages.shape[2]
         _expect(pages, "pages", (R, heads, budget), torch.int32, k_cache)
+        if budget < 1:  # an empty tensor has no address, which the C ABI takes for "every page"
+            raise ValueError("pages must have room for one page at least")
     _ints(R=R, Hq=Hq, max_pages=max_pages, num_pages=num_pages, page_size=page_size, budget=budget)
     out_dtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
     if out_dtype != torch.bfloat16 and out_dtype != torch.float32:

@@ -223,7 +223,9 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t pages = kc->size(0), heads = kc->size(1), P = kc->size(2), D = kc->size(3);
   const int64_t R = table->size(0), width = table->size(1), Hq = q->size(1);
   if (!sized(q, {R, Hq, D}) || !sized(lens, {R}) || Hq % heads != 0) Py_RETURN_NONE;
-  if (a[5] != Py_None && (!(list = plain(a[5], at::kInt, 3, dev)) || list->size(0) != R || list->size(1) != heads)) Py_RETURN_NONE;
+  if (a[5] != Py_None &&
+      (!(list = plain(a[5], at::kInt, 3, dev)) || list->size(0) != R || list->size(1) != heads || list->size(2) < 1))
+    Py_RETURN_NONE;
   const int64_t budget = list ? list->size(2) : 0;
   double scale;
   if (a[7] == Py_None) scale = 1.0 / std::sqrt((double)D);

@@ -280,3 +280,10 @@ def test_select_over_the_widest_tables(cp, kind, R, Hkv, Hq, D, width, budget):
             n = min(budget, held[r])
             want = s.sort(descending=True, stable=True).indices[:n].sort().values.int().cpu()
             assert torch.equal(got[r, h, :n], want) and torch.all(got[r, h, n:] == -1), (r, h)
+
+
+def test_decode_refuses_an_empty_list_of_pages(cp):
+    d = pu.on_gpu(pu.make_cache([30], 2, 1, 64, 16, "bf16", seed=47))
+    for kw in ({}, dict(out_dtype=torch.float32)):
+        with pytest.raises(ValueError, match="pages must have room"):
+            cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], pages=_i32([[[]]]), **kw)

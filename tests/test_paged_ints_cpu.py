@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from long_sequence_context_b200 import cpattn as cp
-from tests.test_paged_cpu import P, _plan_args, _select_args
+from tests.test_paged_cpu import P, _decode_args, _plan_args, _select_args
 
 
 @pytest.mark.parametrize("fn,args,name,good", [(cp.cache_plan, _plan_args, "page_size", P), (cp.cache_plan, _plan_args, "capacity", 4),
@@ -34,3 +34,10 @@ def test_sizes_of_tensors_are_held_to_the_same_limits():
     cp._ints(R=0, Hq=(1 << 31) - 1)
     with pytest.raises(ValueError, match="num_pages"):
         cp._ints(R=3, num_pages=1 << 31)
+
+
+def test_an_empty_list_of_pages_is_not_every_page():
+    a = _decode_args()
+    a["pages"] = torch.zeros((a["q"].shape[0], a["k_cache"].shape[1], 0), dtype=torch.int32)
+    with pytest.raises(ValueError, match="pages must have room"):
+        cp.decode(**a)
