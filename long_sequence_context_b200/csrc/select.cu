@@ -7,7 +7,7 @@
 // in 64 bits, rounded once to fp32: products of 16-bit values are exact there and
 // their sums almost always, so that the order of summation does not decide
 // between near pages.  Beside an infinite bound the second form would multiply it by
-// 0: there the first one is evaluated, with 0 for a zero of q (bound_term).  A head
+// 0: there the first one is evaluated, with 0 for a zero of q (bound_of).  A head
 // whose sum is NaN does not count.  The `budget` pages with the largest scores are listed in
 // ascending order, ties to the lower page; the newest page and the first
 // keep_first pages are always among them.
@@ -102,10 +102,10 @@ template <typename CT, int D>
 __device__ __forceinline__ const CT* bounds_of(const SelectArgs& a, const Pair& p, int page) {
   return static_cast<const CT*>(a.bounds) + ((size_t)page * a.Hkv + p.h) * 2 * D;
 }
-// max(q lo, q hi); NaN if a bound is
-__device__ __forceinline__ double bound_term(float q, float lo, float hi) {
+// What q is multiplied by for max(q lo, q hi), lo <= hi; NaN if a bound is.
+__device__ __forceinline__ float bound_of(float q, float lo, float hi) {
   if (lo != lo || hi != hi) return NAN;
-  return q == 0.f ? 0. : fmax((double)q * lo, (double)q * hi);
+  return q > 0.f ? hi : q < 0.f ? lo : 0.f;
 }
 __device__ __forceinline__ bool in_pool(const SelectArgs& a, int page) { return (unsigned)page < (unsigned)a.num_pages; }
 
@@ -152,7 +152,7 @@ struct Exact {
     const float* b = bounds_of<float, D>(a, p, page);
     const float* q = static_cast<const float*>(a.q) + ((size_t)p.r * a.Hq + (size_t)p.h * a.group + head) * D;
     double sum = 0.;
-    for (int d = 0; d < D; ++d) sum += bound_term(q[d], b[d], b[D + d]);
+    for (int d = 0; d < D; ++d) sum = fma((double)q[d], (double)bound_of(q[d], b[d], b[D + d]), sum);
     return (float)sum;
   }
 
@@ -356,7 +356,10 @@ struct Approx {
     for (int m = h0; m < h1; ++m) {
       double sum = 0.;
 #pragma unroll
-      for (int e = 0; e < V; ++e) sum += bound_term(__bfloat162float(q[(size_t)m * D + e]), lo[e], hi[e]);
+      for (int e = 0; e < V; ++e) {
+        const float x = __bfloat162float(q[(size_t)m * D + e]);
+        sum = fma((double)x, (double)bound_of(x, lo[e], hi[e]), sum);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       key = max(key, order_key((float)sum));
