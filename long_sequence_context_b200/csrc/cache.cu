@@ -317,11 +317,10 @@ constexpr int kAppendWarps = 4;
 constexpr int kTile = 32;  // tokens whose slots one block looks at
 
 // The new rows fall into stretches: tokens next to one another in one page.  A warp
-// takes a stretch of one kv head and copies its runs of consecutive slots one after
-// another, with kAhead rows' loads under way, reduces their keys and writes the page's
-// bounds once: no other warp touches these.  Blocks (x: 32 tokens; y: a share of their
-// stretches and heads) find the stretches that begin in their tokens by a vote over the
-// slots.
+// takes a stretch of one kv head, copies it with kAhead rows' loads under way, 64 tokens
+// with their slots in its lanes at a time, reduces its keys and writes the page's bounds:
+// no other warp touches these.  Blocks (x: 32 tokens; y: a share of their stretches and
+// heads) find the stretches that begin in their tokens by a vote over the slots.
 template <typename IT, typename CT, int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a) {
   constexpr int V = 16 / (int)sizeof(IT);  // elements of a lane
@@ -331,7 +330,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int page_mask = (1 << a.shift) - 1;
   const long long t0 = (long long)blockIdx.x * kTile;
-  const long long mine = t0 + lane < a.N ? a.slots[t0 + lane] : -1;
+  auto slot_of = [&](long long t) { return t < a.N ? a.slots[t] : -1; };
+  const long long mine = slot_of(t0 + lane);
   long long before = __shfl_up_sync(0xffffffffu, mine, 1);
   if (lane == 0) before = t0 > 0 ? a.slots[t0 - 1] : -1;
   const bool bad = mine >= a.n_slots;
@@ -347,61 +347,62 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
   for (int item = blockIdx.y * kAppendWarps + warp; item < items; item += gridDim.y * kAppendWarps) {
     const int stretch = item / a.Hkv, h = item % a.Hkv;
     const int from = __ffs(__ballot_sync(0xffffffffu, first && nth == stretch)) - 1;
-    long long t = t0 + from, slot = __shfl_sync(0xffffffffu, mine, from);
-    const long long page = slot >> a.shift;
-    bool fresh = false;  // the page's first row is among them
+    const long long t = t0 + from, page = __shfl_sync(0xffffffffu, mine, from) >> a.shift;
+    const IT* k = static_cast<const IT*>(a.k) + t * a.k_tok + h * a.k_head + d;
+    const IT* v = static_cast<const IT*>(a.v) + t * a.v_tok + h * a.v_head + d;
+    const size_t at = (((size_t)page * a.Hkv + h) << a.shift) * D + d;  // of the page's first row
+    CT* kc = static_cast<CT*>(a.k_cache) + at;
+    CT* vc = static_cast<CT*>(a.v_cache) + at;
     float lo[V], hi[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) lo[e] = INFINITY, hi[e] = -INFINITY;
-    while (slot >> a.shift == page) {
-      const int off = (int)(slot & page_mask);
-      // the run's length, up to the page's end, and the slot behind it
-      const int most = (int)min((long long)(page_mask + 1 - off), a.N - t);
-      int len;
-      long long next;
-      for (int i = 1;; i += 32) {
-        const long long x = t + i + lane < a.N ? a.slots[t + i + lane] : -1;
-        const uint32_t gap = ~__ballot_sync(0xffffffffu, i + lane < most && x == slot + i + lane);
-        if (gap) {
-          len = i + __ffs(gap) - 1;
-          next = __shfl_sync(0xffffffffu, x, __ffs(gap) - 1);
-          break;
-        }
-      }
-      const IT* k = static_cast<const IT*>(a.k) + t * a.k_tok + h * a.k_head + d;
-      const IT* v = static_cast<const IT*>(a.v) + t * a.v_tok + h * a.v_head + d;
-      const size_t at = ((((size_t)page * a.Hkv + h) << a.shift) + off) * D + d;
-      CT* kc = static_cast<CT*>(a.k_cache) + at;
-      CT* vc = static_cast<CT*>(a.v_cache) + at;
-      for (int i0 = sub; i0 < len; i0 += kRows * kAhead) {
+    bool fresh = false;  // the page's first row is among them
+    long long slot0 = slot_of(t + lane), slot1 = slot_of(t + 32 + lane);
+    for (long long u = t;; u += 64) {
+      const uint32_t other0 = ~__ballot_sync(0xffffffffu, slot0 >> a.shift == page);
+      const uint32_t other1 = ~__ballot_sync(0xffffffffu, slot1 >> a.shift == page);
+      const int n = other0 ? __ffs(other0) - 1 : other1 ? 31 + __ffs(other1) : 64;
+      const int row0 = (int)(slot0 & page_mask), row1 = (int)(slot1 & page_mask);
+      fresh |= (lane < n && row0 == 0) || (lane + 32 < n && row1 == 0);
+      // Rows without a gap are counted: shuffling each out of its lane costs 2 to 5% (5720
+      // tokens of one head in pages of 128: 6.4 us, 6.7 with shuffles, 7.0 in steps of 32).
+      const int from_row = __shfl_sync(0xffffffffu, row0, 0);
+      const bool run = __all_sync(0xffffffffu, (lane >= n || row0 == from_row + lane) &&
+                                                   (lane + 32 >= n || row1 == from_row + 32 + lane));
+      if (n == 64) slot0 = slot_of(u + 64 + lane), slot1 = slot_of(u + 96 + lane);  // under way meanwhile
+#pragma unroll 1
+      for (int i0 = 0; i0 < n; i0 += kRows * kAhead) {
         uint32_t kw[kAhead][4], vw[kAhead][4];
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-          const int i = i0 + x * kRows;
-          if (i < len) {
+          const int i = i0 + x * kRows + sub;
+          if (i < n) {
             load_words(k + i * a.k_tok, kw[x]);
             load_words(v + i * a.v_tok, vw[x]);
           }
         }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-          const int i = i0 + x * kRows;
-          if (i < len) {
+          const int i = i0 + x * kRows + sub;
+          int to = from_row + i;
+          if (!run) to = __shfl_sync(0xffffffffu, i0 < 32 ? row0 : row1, i & 31);
+          if (i < n) {
             float f[V], g[V];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               Unpack<IT>::word(kw[x][w], f + w * Unpack<IT>::kPerWord);
               Unpack<IT>::word(vw[x][w], g + w * Unpack<IT>::kPerWord);
             }
-            put<CT, V>(kc + (size_t)i * D, f, ks);
-            put<CT, V>(vc + (size_t)i * D, g, vs);
+            put<CT, V>(kc + to * D, f, ks);
+            put<CT, V>(vc + to * D, g, vs);
 #pragma unroll
             for (int e = 0; e < V; ++e) lo[e] = fminf(lo[e], f[e]), hi[e] = fmaxf(hi[e], f[e]);
           }
         }
       }
-      fresh |= off == 0;
-      t += len, slot = next;
+      if (n < 64) break;
+      k += 64 * a.k_tok;
+      v += 64 * a.v_tok;
     }
     if (!a.bounds) continue;
 #pragma unroll
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendA
         lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
         hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
       }
+    fresh = __any_sync(0xffffffffu, fresh);
     if (sub != 0) continue;
     CT* b = static_cast<CT*>(a.bounds) + ((size_t)page * a.Hkv + h) * 2 * D + d;
     if (!fresh) {  // the page held rows before: its first row starts its bounds afresh

@@ -287,3 +287,40 @@ def test_decode_refuses_an_empty_list_of_pages(cp):
     for kw in ({}, dict(out_dtype=torch.float32)):
         with pytest.raises(ValueError, match="pages must have room"):
             cp.decode(d["q"], d["k"], d["v"], d["table"], d["lens"], pages=_i32([[[]]]), **kw)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3"])
+@pytest.mark.parametrize("D,P", [(64, 256), (128, 128), (64, 16)])
+def test_append_runs_of_every_length_and_start(cp, kind, D, P):
+    """Consecutive rows from and to any row, with and without one gap, beside the steps of 32 and 64 tokens."""
+    g = torch.Generator().manual_seed(D * P)
+    am = torch.tensor([6.0, 6.0], device="cuda") if kind == "e4m3" else None
+    starts = [0, 1, 15] if P == 16 else [0, 1, 31, 32, 33, 63, 64, 65, P - 2, P - 1]
+    ends = [s + n for s in starts for n in (1, 31, 32, 33, 63, 64, 65, 127, 128, 129, P)]
+    runs = sorted({(s, min(e, P)) for s, e in zip([s for s in starts for _ in range(11)], ends)})
+    slots = []
+    for p, (lo, hi) in enumerate(runs + runs):
+        rows = list(range(lo, hi))
+        if p >= len(runs) and len(rows) > 2:
+            rows.pop(int(torch.randint(1, len(rows) - 1, (1,), generator=g)))
+        slots += [p * P + i for i in rows]
+    n_pages = 2 * len(runs)
+    k = torch.zeros((n_pages, 2, P, D), dtype=pu.DTYPES[kind], device="cuda")
+    v, b = k.clone(), torch.zeros((n_pages, 2, 2, D), dtype=pu.DTYPES[kind], device="cuda")
+    rows = [torch.randn(len(slots), 2, D, generator=g).to(pu.rows_dtype(kind)) for _ in range(2)]
+    for bounds in (None, b):
+        k.zero_(), v.zero_()
+        cp.cache_append_(rows[0].cuda(), rows[1].cuda(), torch.tensor(slots, device="cuda"), k, v, k_bounds=bounds, kv_amax=am)
+        assert cp.sync_status() == cp.OK
+        put = [fp8.decode(pu.codes_of(x, 6.0)) if kind == "e4m3" else pu.values(x) for x in rows]
+        for got, x in ((k, put[0]), (v, put[1])):
+            want = np.zeros((n_pages * P, 2, D))
+            want[slots] = x
+            assert np.array_equal(pu.values(got), want.reshape(n_pages, P, 2, D).transpose(0, 2, 1, 3))
+    bv, page_of = pu.values(b), np.array(slots) // P
+    for p in range(n_pages):
+        mine = put[0][page_of == p]
+        lo, hi = mine.min(0), mine.max(0)
+        if p * P not in slots:  # it goes on from the zeros
+            lo, hi = np.minimum(lo, 0), np.maximum(hi, 0)
+        assert np.array_equal(bv[p, :, 0], lo) and np.array_equal(bv[p, :, 1], hi)
