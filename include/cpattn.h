@@ -347,9 +347,10 @@ int cpattn_gemm(const void* A, const void* B, const void* bias, void* C, int M, 
  *   slot              page * page_size + row, int64: where one token's rows stand
  * Positions behind a request's length may hold anything, NaN included: they are
  * never part of a result.  R requests of which some have length 0 are a padded
- * batch.  A page number, slot or length outside of its range is not followed:
- * the rows it stands for are left out and CPATTN_ERR_PAGE is recorded in the
- * device error word (cpattn_sync_status).  All sizes are read on the device, so
+ * batch.  A page number or slot outside of its range is not followed: the rows it
+ * stands for are left out; of a length below 0 or above max_pages * page_size
+ * cpattn_select_pages and cpattn_decode take that limit; and CPATTN_ERR_PAGE is
+ * recorded in the device error word (cpattn_sync_status).  All sizes are read on the device, so
  * every call can be captured into a CUDA graph and replayed as lengths change.
  * Limits (CPATTN_ERR_SHAPE): max_pages * page_size < 2^31, at most 64 query
  * heads per kv head (Hq % Hkv == 0).
@@ -453,6 +454,10 @@ int cpattn_select_pages(const void* q, const void* k_bounds, const int32_t* bloc
  *                  Requests without a key: o = 0, lse = -inf.  fp32 results of
  *                  parts of one context (kept by several ranks) are combined by
  *                  cpattn_merge and rounded by cpattn_finalize
+ * Scores, maxima and sums are fp32.  With bf16 and e4m3 caches a weight enters the
+ * weighted sum as two 16-bit numbers, off by 2^-17 (bf16) or 2^-22 (e4m3) relative:
+ * nothing in a bf16 result, the largest error of an fp32 one.  Keys and values are
+ * finite numbers: one that is infinite or NaN makes its heads' results NaN or infinite.
  * Workspace: cpattn_decode_workspace_bytes(R, Hq, Hkv, D) (0 for invalid sizes),
  * 256-byte aligned; contents on entry are ignored; calls that can overlap on the
  * GPU need one each.  Results do not depend on it, nor on other requests' values.

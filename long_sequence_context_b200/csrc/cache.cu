@@ -4,13 +4,13 @@
 // or tokens taken back) the pages they take from and return to the pool, the
 // new tokens' slots and the lengths afterwards.  Integer work of a few bytes
 // per request and token: the launch and the prefix sums' latency bound it (16
-// requests: 3 us; 512 with 116,000 tokens: 7 us).
+// requests: 2.9 us; 512 with 116,000 tokens: 5.1 us).
 //
 // cache_append: new K and V rows into their slots, quantised for an 8-bit
 // cache, with the elementwise smallest and largest key of every page kept up
 // to date.  Every row is read and written once: the memory bandwidth bounds it
 // (8192 tokens x 16 heads x 128 bf16, 135 MB: 25.5 us, 5.3 TB/s, 0.82 of a plain
-// copy).
+// copy; in fp32, 268 MB, 52 us; to e4m3, 101 MB, 20.5).
 #include <algorithm>
 
 #include "cpattn.h"

@@ -21,9 +21,11 @@
 // us, 6.4 TB/s; 131072 x 8 heads in e4m3, where the codes' widening doubles the
 // instructions for a byte: 268 MB in 49 us), beside some 6 us of start, partial
 // results and join.  Short contexts wait for a chain of latencies (launch, length,
-// page, keys, join): 16 keys take 3.7 to 4.8 us, 257 keys x 16 heads 5.0.  Groups of 32
-// heads wait for their instructions (268 MB in 70 us); sharing a ring between the warps
-// of a group took longer (77).
+// page, keys, join): 16 keys take 3.7 to 4.8 us, 257 keys x 16 heads 5.0.  Many heads a
+// group wait for their instructions with two warps a scheduler: 268 MB with 32 heads take
+// 66 us in bf16 (tensor pipe 38% busy, issue slots 37%), with 16 heads 56 in e4m3 (45%,
+// 37%) and 97 in fp32 (FMA pipe 34%, issue slots 50%).  Sharing a ring between the warps
+// of a group of 32 took longer (77 us for 70 at the time).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -264,10 +266,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // little.  A lane's 16 bytes of consecutive columns are at once its share of one
 // or more operands (the contraction index may be permuted at will).  8-bit codes
 // are widened to half precision, which holds them exactly; the queries then are
-// in half precision too, scaled per head by a power of two so that none of their
-// bits is lost.  The weights enter as the sum of two 16-bit numbers (2^-17
-// relative or better): the kernel waits for memory, the second product is free,
-// and fp32 outputs stay good to that.
+// in half precision too, scaled per head by a power of two: entries down to 2^-31 of
+// the head's largest keep all their bits, smaller ones are off by 2^-39 of it at most.
+// The weights enter as the sum of two 16-bit numbers, off by at most 2^-17 relative in
+// bf16 and by 2^-22, or 2^-39 of the largest weight, in half precision: the kernel waits
+// for memory, the second product is free, and fp32 outputs stay good to that.
 template <typename C, int D, int NT>
 struct MmaTile {
   using CT = C;

@@ -22,11 +22,15 @@
 // One cluster of thread blocks takes one (request, kv head): every block scores
 // a stretch of pages and sends the scores to the first block's shared memory,
 // which finds the threshold by a radix search of eight bits at a time and lists
-// the pages.  A page's bounds are read once; what bounds the kernel is the
-// chain of latencies from the lengths over the page table and the bounds to the
-// search, so the pages are spread over as many blocks as the device holds at once.
-// Measured (8 kv heads, 4 query heads each, D = 128, us): 2048 pages 11.0, 8192
-// pages 24.4 (33.8 with every page scored in 64 bits), 16 x 8192 pages 118 (197).
+// the pages.  A page's bounds are read once.  What bounds one request is the chain of
+// latencies from the lengths over the page table and the bounds to the search, so the
+// pages are spread over as many blocks as the device holds at once.  In a batch it is the
+// scoring: a warp asks for a step's page numbers, then for its bounds, and only then
+// multiplies (of some 11 cycles that a warp takes for an instruction 5.9 are waits for
+// memory, which runs at 0.7 of a copy).  fp32 bounds are all scored in 64 bits.
+// Measured (8 kv heads, 4 query heads each, D = 128, us; bf16 | e4m3 | fp32): 2048 pages
+// 10.4 | 10.4 | 12.4, 8192 pages 25.3 | 24.0 | 37, 16 x 8192 pages 117 | 110 | 252 (bf16
+// with every page scored in 64 bits: 33.8 for 8192 pages, 197 for 16 x 8192).
 #include <cooperative_groups.h>
 
 #include <algorithm>
