@@ -457,9 +457,8 @@ int cpattn_select_pages(const void* q, const void* k_bounds, const int32_t* bloc
  * Scores, maxima and sums are fp32.  With bf16 and e4m3 caches a weight enters the
  * weighted sum as two 16-bit numbers, off by 2^-17 (bf16) or 2^-22 (e4m3; or 2^-39 of
  * the head's largest weight) relative: nothing in a bf16 result, the largest error of
- * an fp32 one.  Queries, keys, values
- * and q . k before it is scaled are finite in fp32: a key or value that is infinite or
- * NaN makes its heads' results NaN or infinite.
+ * an fp32 one.  Queries, keys, values and q . k before it is scaled are finite in fp32:
+ * a key or value that is infinite or NaN makes its heads' results NaN or infinite.
  * Workspace: cpattn_decode_workspace_bytes(R, Hq, Hkv, D) (0 for invalid sizes),
  * 256-byte aligned; contents on entry are ignored; calls that can overlap on the
  * GPU need one each.  Results do not depend on it, nor on other requests' values.
